@@ -311,6 +311,162 @@ moe_status_t moe_layer_capped(const float* logits, const void* x, moe_dtype_t ac
                               void* x_sorted, float* y_sorted, void* y, moe_dtype_t y_dtype,
                               void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * ---------------------------------------------------------------------------------------
+ * Training: the pieces of the layer's gradient
+ * ---------------------------------------------------------------------------------------
+ * The forward pass of a trained layer is moe_route, moe_permute, two moe_grouped_gemm (gate and
+ * up), moe_swiglu, a third moe_grouped_gemm (down) and moe_combine; its backward pass goes back
+ * through moe_combine_backward, moe_grouped_gemm_dgrad and _wgrad (down), moe_swiglu_backward,
+ * dgrad and wgrad (gate and up), moe_permute_backward and moe_route_backward. What the backward
+ * pass needs of the forward pass can be held in 8 bits (moe_checkpoint_pack, moe_swiglu).
+ *
+ * In all of them d, d_ff, N and K are multiples of 8 and at most 2^20 (MOE_ERR_UNSUPPORTED /
+ * MOE_ERR_INVALID_ARG otherwise), element counts may pass 2^31, and a size whose kernels would
+ * need more than 2^31 - 1 workgroups gives MOE_ERR_UNSUPPORTED. Rows at or past offsets[E]
+ * (kept rows after moe_permute_capped) are neither read nor written. Results in MOE_BF16 are
+ * the fp32 result rounded once, to nearest even. None of these calls needs a workspace.
+ */
+
+/*
+ * moe_grouped_gemm - one matrix product per expert over its contiguous rows (the same grouped
+ * GEMM as moe_grouped_ffn's, tutorial page, section 4, compute, without the activation):
+ *     y[r] = W_e x[r]    for rows r in [offsets[e], offsets[e+1])
+ *
+ *   x        [rows, K] in x_dtype (MOE_BF16 or MOE_F32).
+ *   offsets  [E+1] int32, as moe_grouped_ffn; offsets[E] <= rows.
+ *   w        [E, N, K] in w_dtype = x_dtype, row-major (contraction axis contiguous). Experts
+ *            with no rows are never read.
+ *   y        [rows, N] out, in y_dtype (MOE_F32 or MOE_BF16).
+ *   Arithmetic: the products are summed in fp32.
+ */
+moe_status_t moe_grouped_gemm(const void* x, moe_dtype_t x_dtype, const int32_t* offsets, int rows,
+                              int E, int N, int K, const void* w, moe_dtype_t w_dtype, void* y,
+                              moe_dtype_t y_dtype, void* stream);
+
+/*
+ * moe_grouped_gemm_dgrad - its gradient with respect to x:
+ *     dx[r] = W_e^T dy[r]  (+ W2_e^T dy2[r])
+ *
+ *   dy       [rows, N] in dy_dtype; dy2: a second gradient of the same shape, or NULL.
+ *   w        [E, N, K] in w_dtype = dy_dtype, the forward product's weights as they are stored;
+ *            w2: those of dy2, NULL exactly when dy2 is. Both products go into one fp32 sum
+ *            (x feeds gate and up alike).
+ *   dx       [rows, K] out, in dx_dtype (MOE_F32 or MOE_BF16).
+ */
+moe_status_t moe_grouped_gemm_dgrad(const void* dy, const void* dy2, moe_dtype_t dy_dtype,
+                                    const int32_t* offsets, int rows, int E, int N, int K,
+                                    const void* w, const void* w2, moe_dtype_t w_dtype, void* dx,
+                                    moe_dtype_t dx_dtype, void* stream);
+
+/*
+ * moe_grouped_gemm_wgrad - its gradient with respect to the weights:
+ *     dW_e = sum over the expert's rows of dy[r] x[r]^T
+ *
+ *   dy, x       [rows, N] and [rows, K] in dtype (MOE_BF16 or MOE_F32).
+ *   dw          [E, N, K] out, in dw_dtype (MOE_F32 or MOE_BF16). With accumulate = 0 every
+ *               element is written (zeros for an expert with no rows); with accumulate = 1 the
+ *               sum is added to what dw holds (in fp32, rounded once to dw_dtype) and experts
+ *               with no rows keep theirs. Other values of accumulate: MOE_ERR_INVALID_ARG.
+ */
+moe_status_t moe_grouped_gemm_wgrad(const void* dy, const void* x, moe_dtype_t dtype,
+                                    const int32_t* offsets, int rows, int E, int N, int K, void* dw,
+                                    moe_dtype_t dw_dtype, int accumulate, void* stream);
+
+/*
+ * Held rows. A row of d elements is held as d fp8 e4m3fn codes and ceil(d/128) fp32 scales, one
+ * per 128 consecutive elements (the last group of a row may be shorter); an element's value is
+ * code * scale. The scale is the smallest power of two with which the group's largest finite
+ * magnitude is at most 448, and between 2^-117 and 2^120 (1 for a group of zeros), so values
+ * are exact in bf16 and the one rounding is the code's, to nearest even: at most 2^-4 of the
+ * element, or 2^-10 of the scale for elements under 2^-6 of it. (At scale 2^120 codes stop
+ * at 240.) NaN and infinities are held as NaN and do not enter the scale.
+ */
+
+/*
+ * moe_checkpoint_pack - hold rows in 8 bits.
+ *   x [rows, d] in x_dtype (MOE_BF16 or MOE_F32); codes [rows, d] bytes out;
+ *   scales [rows, ceil(d/128)] fp32 out.
+ */
+moe_status_t moe_checkpoint_pack(const void* x, moe_dtype_t x_dtype, int rows, int d, void* codes,
+                                 float* scales, void* stream);
+
+/*
+ * moe_checkpoint_unpack - held rows back as values, in token order or gathered into
+ * expert-sorted order (so that a layer's input is held once per token, not once per row).
+ *   codes [T, d], scales [T, ceil(d/128)] as written by moe_checkpoint_pack or moe_swiglu.
+ *   flat_to_sorted [T, k] int32 or NULL (then k must be 1).
+ *   out [T*k, d] in out_dtype (MOE_BF16 or MOE_F32):
+ *       out[flat_to_sorted[t*k + j]] = row t (entries outside [0, T*k), dropped assignments,
+ *       are skipped, and rows that no entry names are left as they were); out[t] = row t
+ *       without a map.
+ */
+moe_status_t moe_checkpoint_unpack(const void* codes, const float* scales, int T, int k, int d,
+                                   const int32_t* flat_to_sorted, void* out, moe_dtype_t out_dtype,
+                                   void* stream);
+
+/*
+ * moe_swiglu - h = silu(g) * u, and g and u held in 8 bits for the backward pass.
+ *   g, u     [rows, d_ff] in dtype (MOE_BF16 or MOE_F32); h [rows, d_ff] out, in dtype.
+ *   offsets  [E+1] int32: only rows below offsets[E] (at most rows) are worked on; NULL: all
+ *            rows (E is then not used).
+ *   g_codes, u_codes [rows, d_ff] bytes out, g_scales, u_scales [rows, ceil(d_ff/128)] fp32 out:
+ *            all four, or all NULL.
+ */
+moe_status_t moe_swiglu(const void* g, const void* u, moe_dtype_t dtype, const int32_t* offsets,
+                        int E, int rows, int d_ff, void* h, void* g_codes, float* g_scales,
+                        void* u_codes, float* u_scales, void* stream);
+
+/*
+ * moe_swiglu_backward - with s = 1 / (1 + e^-g):
+ *     du = dh g s,   dg = dh u s (1 + g (1 - s)),   h = g s u
+ *   dh       [rows, d_ff] in dtype (MOE_BF16 or MOE_F32); dg, du out and h out (or NULL), same
+ *            shape and dtype. h is the forward result again, for the down projection's weight
+ *            gradient.
+ *   g, u     [rows, d_ff] in gu_dtype: dtype (scales NULL), or MOE_FP8_E4M3FN, codes with
+ *            their scales g_scales, u_scales [rows, ceil(d_ff/128)].
+ *   offsets, E as moe_swiglu.
+ */
+moe_status_t moe_swiglu_backward(const void* dh, moe_dtype_t dtype, const void* g, const void* u,
+                                 moe_dtype_t gu_dtype, const float* g_scales,
+                                 const float* u_scales, const int32_t* offsets, int E, int rows,
+                                 int d_ff, void* dg, void* du, void* h, void* stream);
+
+/*
+ * moe_combine_backward - the gradients of moe_combine. For p = flat_to_sorted[t*k + j]:
+ *     dy_sorted[p] = topk_gates[t, j] * dy[t],   dgates[t, j] = sum_i dy[t, i] y_sorted[p, i]
+ *   dy         [T, d] in dy_dtype (MOE_BF16 or MOE_F32).
+ *   y_sorted   [T*k, d] fp32 (moe_combine's input); flat_to_sorted, topk_gates as moe_combine.
+ *   dy_sorted  [T*k, d] out, in dys_dtype (MOE_BF16 or MOE_F32); rows that no entry names are
+ *              left as they were.
+ *   dgates     [T, k] fp32 out, 0 for dropped assignments; summed in fp32. NULL exactly when
+ *              y_sorted is (gates that are not trained).
+ */
+moe_status_t moe_combine_backward(const void* dy, moe_dtype_t dy_dtype, const float* y_sorted,
+                                  const int32_t* flat_to_sorted, const float* topk_gates, int T,
+                                  int k, int d, void* dy_sorted, moe_dtype_t dys_dtype,
+                                  float* dgates, void* stream);
+
+/*
+ * moe_permute_backward - the gradient of moe_permute's row copy: dx[t] is the sum of the rows
+ * flat_to_sorted[t*k + j], j = 0..k-1, of dx_sorted, in fp32 and slot order; dropped
+ * assignments add nothing.
+ *   dx_sorted [T*k, d] in dtype, dx [T, d] out in dx_dtype (each MOE_BF16 or MOE_F32).
+ */
+moe_status_t moe_permute_backward(const void* dx_sorted, moe_dtype_t dtype,
+                                  const int32_t* flat_to_sorted, int T, int k, int d, void* dx,
+                                  moe_dtype_t dx_dtype, void* stream);
+
+/*
+ * moe_route_backward - the gradient of moe_route's gates with respect to the logits:
+ *     dlogits[t, topk_ids[t, j]] = g_j (dgates[t, j] - sum_i g_i dgates[t, i]),  g = topk_gates[t]
+ *   and 0 for the experts that token t does not go to.
+ *   dgates, topk_gates [T, k] fp32, topk_ids [T, k] int32, dlogits [T, E] fp32 out.
+ */
+moe_status_t moe_route_backward(const float* dgates, const int32_t* topk_ids,
+                                const float* topk_gates, int T, int E, int k, float* dlogits,
+                                void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -8,5 +8,7 @@ from .binding import (  # noqa: F401
     MoeError, Workspace, library_path, load_library, moe_combine, moe_grouped_ffn, moe_layer,
     moe_layer_workspace_size, moe_ffn_workspace_size, moe_permute, moe_permute_workspace_size,
     moe_route, moe_expert_capacity, moe_route_gemm, moe_route_gemm_workspace_size,
-    moe_block_weights,
+    moe_block_weights, moe_checkpoint_pack, moe_checkpoint_unpack, moe_combine_backward,
+    moe_grouped_gemm, moe_grouped_gemm_dgrad, moe_grouped_gemm_wgrad, moe_permute_backward,
+    moe_route_backward, moe_swiglu, moe_swiglu_backward,
 )

@@ -29,6 +29,9 @@ ENTRY_POINTS = (
     "moe_layer", "moe_expert_capacity", "moe_permute_capped", "moe_layer_capped",
     "moe_route_gemm", "moe_route_gemm_workspace_size", "moe_permute_noalloc",
     "moe_block_weights",
+    "moe_grouped_gemm", "moe_grouped_gemm_dgrad", "moe_grouped_gemm_wgrad", "moe_checkpoint_pack",
+    "moe_checkpoint_unpack", "moe_swiglu", "moe_swiglu_backward", "moe_combine_backward",
+    "moe_permute_backward", "moe_route_backward",
 )
 
 _lib = None
@@ -73,6 +76,16 @@ def load_library(path: str | None = None):
         "moe_block_weights": ([P, P, I, I, I, I, P], I),
         "moe_layer_capped": ([P, P, I, I, I, I, I, I, I, P, P, P, I, P, P, P,
                               P, P, P, P, P, P, P, P, P, I, P, S, P], I),
+        "moe_grouped_gemm": ([P, I, P, I, I, I, I, P, I, P, I, P], I),
+        "moe_grouped_gemm_dgrad": ([P, P, I, P, I, I, I, I, P, P, I, P, I, P], I),
+        "moe_grouped_gemm_wgrad": ([P, P, I, P, I, I, I, I, P, I, I, P], I),
+        "moe_checkpoint_pack": ([P, I, I, I, P, P, P], I),
+        "moe_checkpoint_unpack": ([P, P, I, I, I, P, P, I, P], I),
+        "moe_swiglu": ([P, P, I, P, I, I, I, P, P, P, P, P, P], I),
+        "moe_swiglu_backward": ([P, I, P, P, I, P, P, P, I, I, I, P, P, P, P], I),
+        "moe_combine_backward": ([P, I, P, P, P, I, I, I, P, I, P, P], I),
+        "moe_permute_backward": ([P, I, P, I, I, I, P, I, P], I),
+        "moe_route_backward": ([P, P, P, I, I, I, P, P], I),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -339,6 +352,198 @@ def moe_layer(logits, x, w_gate, w_up, w_down, k: int, out: dict, workspace: Wor
         _check(lib.moe_layer(*head, *tail))
     else:
         _check(lib.moe_layer_capped(*head, int(capacity), *tail))
+
+
+# ----------------------------------------------------------------------------------------
+# training: the pieces of the layer's gradient (same names as the C ABI)
+# ----------------------------------------------------------------------------------------
+def _call(name: str, stream, tensors, args):
+    """Enqueue lib.<name>(*args, stream) on the device that every tensor is on, whichever is
+    current: on `stream`, or on that device's current stream."""
+    ptrs = {id(t): _ptr(t) for t in tensors if t is not None}
+    devices = {t.device for t in tensors if t is not None}
+    if len(devices) != 1:
+        raise ValueError("expected every tensor on one device")
+    device = devices.pop()
+    if stream is not None and stream.device != device:
+        raise ValueError("expected a stream of the tensors' device")
+    with torch.cuda.device(device):
+        if stream is None:
+            stream = torch.cuda.current_stream()
+        _check(getattr(load_library(), name)(*[ptrs[id(a)] if isinstance(a, torch.Tensor) else a for a in args],
+                                             _stream(stream)))
+
+
+def _float_dt(t, name):
+    if t.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"{name}: expected float32 or bfloat16, got {t.dtype}")
+    return _DTYPE_ENUM[t.dtype]
+
+
+def _dims(t, n, name):
+    if t.dim() != n:
+        raise ValueError(f"{name}: expected {n} dimensions, got shape {tuple(t.shape)}")
+    return t.shape
+
+
+def _held(codes, scales, shape, name):
+    """codes (float8_e4m3fn or uint8) and scales of rows held in 8 bits."""
+    if codes.dtype not in (torch.float8_e4m3fn, torch.uint8):
+        raise TypeError(f"{name}_codes: expected float8_e4m3fn or uint8, got {codes.dtype}")
+    _need(codes, codes.dtype, shape, f"{name}_codes")
+    _need(scales, torch.float32, (shape[0], -(-shape[1] // 128)), f"{name}_scales")
+
+
+def moe_grouped_gemm(x, offsets, w, y, stream=None):
+    """y[r] = W_e x[r] for the rows of each expert e. x [rows, K] and w [E, N, K] in one dtype
+    (bfloat16 or float32), y [rows, N] float32 or bfloat16."""
+    rows, K = _dims(x, 2, "x")
+    E, N, _ = _dims(w, 3, "w")
+    _need(w, x.dtype, (E, N, K), "w")
+    _need(offsets, torch.int32, (E + 1,), "offsets")
+    _need(y, y.dtype, (rows, N), "y")
+    _call("moe_grouped_gemm", stream, (x, offsets, w, y),
+          (x, _float_dt(x, "x"), offsets, rows, E, N, K, w, _float_dt(w, "w"), y, _float_dt(y, "y")))
+
+
+def moe_grouped_gemm_dgrad(dy, offsets, w, dx, dy2=None, w2=None, stream=None):
+    """dx[r] = W_e^T dy[r], plus W2_e^T dy2[r] with dy2 and w2. dy [rows, N] and w [E, N, K] in one
+    dtype (bfloat16 or float32), dx [rows, K] float32 or bfloat16."""
+    rows, N = _dims(dy, 2, "dy")
+    E, _, K = _dims(w, 3, "w")
+    _need(w, dy.dtype, (E, N, K), "w")
+    _need(offsets, torch.int32, (E + 1,), "offsets")
+    _need(dx, dx.dtype, (rows, K), "dx")
+    if (dy2 is None) != (w2 is None):
+        raise ValueError("dy2 and w2 come together")
+    if dy2 is not None:
+        _need(dy2, dy.dtype, (rows, N), "dy2")
+        _need(w2, dy.dtype, (E, N, K), "w2")
+    _call("moe_grouped_gemm_dgrad", stream, (dy, dy2, offsets, w, w2, dx),
+          (dy, dy2, _float_dt(dy, "dy"), offsets, rows, E, N, K, w, w2, _float_dt(w, "w"), dx,
+           _float_dt(dx, "dx")))
+
+
+def moe_grouped_gemm_wgrad(dy, x, offsets, dw, accumulate: bool = False, stream=None):
+    """dw[e] = sum over expert e's rows of dy[r] x[r]^T, or dw[e] += with accumulate. dy [rows, N] and
+    x [rows, K] in one dtype (bfloat16 or float32), dw [E, N, K] float32 or bfloat16."""
+    rows, N = _dims(dy, 2, "dy")
+    _, K = _dims(x, 2, "x")
+    E = _dims(dw, 3, "dw")[0]
+    _need(x, dy.dtype, (rows, K), "x")
+    _need(offsets, torch.int32, (E + 1,), "offsets")
+    _need(dw, dw.dtype, (E, N, K), "dw")
+    _call("moe_grouped_gemm_wgrad", stream, (dy, x, offsets, dw),
+          (dy, x, _float_dt(dy, "dy"), offsets, rows, E, N, K, dw, _float_dt(dw, "dw"), int(bool(accumulate))))
+
+
+def moe_checkpoint_pack(x, codes, scales, stream=None):
+    """Hold x [rows, d] (bfloat16 or float32) in 8 bits: codes [rows, d] (float8_e4m3fn or uint8) and
+    scales [rows, ceil(d/128)] float32."""
+    rows, d = _dims(x, 2, "x")
+    _held(codes, scales, (rows, d), "x")
+    _call("moe_checkpoint_pack", stream, (x, codes, scales), (x, _float_dt(x, "x"), rows, d, codes, scales))
+
+
+def moe_checkpoint_unpack(codes, scales, out, flat_to_sorted=None, stream=None):
+    """Held rows back as values: out [T, d], or with flat_to_sorted [T*k] out [T*k, d], where row t
+    goes to each of its k sorted rows (bfloat16 or float32)."""
+    T, d = _dims(codes, 2, "codes")
+    _held(codes, scales, (T, d), "x")
+    rows = T if flat_to_sorted is None else flat_to_sorted.numel()
+    if flat_to_sorted is not None:
+        _need(flat_to_sorted, torch.int32, (rows,), "flat_to_sorted")
+    if T and rows % T:
+        raise ValueError("flat_to_sorted must have k entries for every row")
+    _need(out, out.dtype, (rows, d), "out")
+    _call("moe_checkpoint_unpack", stream, (codes, scales, flat_to_sorted, out),
+          (codes, scales, T, rows // T if T else 1, d, flat_to_sorted, out, _float_dt(out, "out")))
+
+
+def moe_swiglu(g, u, h, g_codes=None, g_scales=None, u_codes=None, u_scales=None, offsets=None, stream=None):
+    """h = silu(g) * u, all [rows, d_ff] in one dtype (bfloat16 or float32); with codes and scales, g
+    and u are held in 8 bits too. offsets [E+1]: only rows below offsets[E]."""
+    rows, f = _dims(g, 2, "g")
+    _need(u, g.dtype, (rows, f), "u")
+    _need(h, g.dtype, (rows, f), "h")
+    held = (g_codes, g_scales, u_codes, u_scales)
+    if any(t is not None for t in held):
+        if any(t is None for t in held):
+            raise ValueError("g_codes, g_scales, u_codes and u_scales come together")
+        _held(g_codes, g_scales, (rows, f), "g")
+        _held(u_codes, u_scales, (rows, f), "u")
+    E = _row_offsets(offsets)
+    _call("moe_swiglu", stream, (g, u, offsets, h, *held),
+          (g, u, _float_dt(g, "g"), offsets, E, rows, f, h, *held))
+
+
+def _row_offsets(offsets) -> int:
+    if offsets is None:
+        return 0
+    E = offsets.numel() - 1
+    _need(offsets, torch.int32, (E + 1,), "offsets")
+    return E
+
+
+def moe_swiglu_backward(dh, g, u, dg, du, h=None, g_scales=None, u_scales=None, offsets=None, stream=None):
+    """dg and du (and h again, if given) from dh, all [rows, d_ff] in dh's dtype; g and u in that dtype,
+    or held in 8 bits (codes, with g_scales and u_scales)."""
+    rows, f = _dims(dh, 2, "dh")
+    for t, n in ((dg, "dg"), (du, "du"), (h, "h")):
+        if t is not None:
+            _need(t, dh.dtype, (rows, f), n)
+    if g_scales is None and u_scales is None:
+        _need(g, dh.dtype, (rows, f), "g")
+        _need(u, dh.dtype, (rows, f), "u")
+        gu = _float_dt(g, "g")
+    elif g_scales is None or u_scales is None:
+        raise ValueError("g_scales and u_scales come together")
+    else:
+        _held(g, g_scales, (rows, f), "g")
+        _held(u, u_scales, (rows, f), "u")
+        gu = MOE_FP8_E4M3FN
+    E = _row_offsets(offsets)
+    _call("moe_swiglu_backward", stream, (dh, g, u, g_scales, u_scales, offsets, dg, du, h),
+          (dh, _float_dt(dh, "dh"), g, u, gu, g_scales, u_scales, offsets, E, rows, f, dg, du, h))
+
+
+def moe_combine_backward(dy, y_sorted, flat_to_sorted, topk_gates, dy_sorted, dgates, stream=None):
+    """dy_sorted [T*k, d] and dgates [T, k] (float32) from dy [T, d]; dy and dy_sorted float32 or
+    bfloat16. y_sorted and dgates None together: dy_sorted alone."""
+    T, d = _dims(dy, 2, "dy")
+    k = _dims(topk_gates, 2, "topk_gates")[1]
+    _need(topk_gates, torch.float32, (T, k), "topk_gates")
+    _need(flat_to_sorted, torch.int32, (T * k,), "flat_to_sorted")
+    _need(dy_sorted, dy_sorted.dtype, (T * k, d), "dy_sorted")
+    if (y_sorted is None) != (dgates is None):
+        raise ValueError("y_sorted and dgates come together")
+    if dgates is not None:
+        _need(y_sorted, torch.float32, (T * k, d), "y_sorted")
+        _need(dgates, torch.float32, (T, k), "dgates")
+    _call("moe_combine_backward", stream, (dy, y_sorted, flat_to_sorted, topk_gates, dy_sorted, dgates),
+          (dy, _float_dt(dy, "dy"), y_sorted, flat_to_sorted, topk_gates, T, k, d, dy_sorted,
+           _float_dt(dy_sorted, "dy_sorted"), dgates))
+
+
+def moe_permute_backward(dx_sorted, flat_to_sorted, k: int, dx, stream=None):
+    """dx[t] = sum of the k rows of dx_sorted that token t went to (float32 or bfloat16 each)."""
+    T, d = _dims(dx, 2, "dx")
+    _need(dx_sorted, dx_sorted.dtype, (T * k, d), "dx_sorted")
+    _need(flat_to_sorted, torch.int32, (T * k,), "flat_to_sorted")
+    _call("moe_permute_backward", stream, (dx_sorted, flat_to_sorted, dx),
+          (dx_sorted, _float_dt(dx_sorted, "dx_sorted"), flat_to_sorted, T, k, d, dx, _float_dt(dx, "dx")))
+
+
+def moe_route_backward(dgates, topk_ids, topk_gates, dlogits, stream=None):
+    """dlogits [T, E] (all of it) from dgates [T, k], the gradient of moe_route's gates."""
+    T, k = _dims(dgates, 2, "dgates")
+    E = _dims(dlogits, 2, "dlogits")[1]
+    _need(dgates, torch.float32, (T, k), "dgates")
+    _need(topk_ids, torch.int32, (T, k), "topk_ids")
+    _need(topk_gates, torch.float32, (T, k), "topk_gates")
+    _need(dlogits, torch.float32, (T, E), "dlogits")
+    _call("moe_route_backward", stream, (dgates, topk_ids, topk_gates, dlogits),
+          (dgates, topk_ids, topk_gates, T, E, k, dlogits))
 
 
 def layer_buffers(T: int, E: int, k: int, d: int, act_dtype, device="cuda",

@@ -182,6 +182,57 @@ moe_status_t check_combine(const float* y_sorted, const int32_t* f2s, const floa
   return MOE_OK;
 }
 
+// ---- training ----
+constexpr long long kMaxGrid = 0x7fffffffLL;
+
+bool float_dtype(moe_dtype_t t) { return t == MOE_F32 || t == MOE_BF16; }
+// MOE_OK for the two formats of activations and gradients, else why not
+moe_status_t check_float_dtype(moe_dtype_t t) {
+  if (float_dtype(t)) return MOE_OK;
+  return t >= MOE_FP8_E4M3FN && t <= MOE_FP8_E4M3FN_BLOCKED ? MOE_ERR_UNSUPPORTED : MOE_ERR_INVALID_ARG;
+}
+moe_status_t check_width(int d) {
+  if (d < 1 || d > kMaxDim) return MOE_ERR_INVALID_ARG;
+  return d % 8 == 0 ? MOE_OK : MOE_ERR_UNSUPPORTED;
+}
+long long held_groups(int d) { return (d + 127) / 128; }
+
+// offsets of the row-wise calls: NULL (all rows) or [E + 1]
+moe_status_t check_row_offsets(const int32_t* offsets, int E) {
+  if (!offsets) return MOE_OK;
+  if (E < 1 || !aligned(offsets, 4)) return MOE_ERR_INVALID_ARG;
+  return E > MOE_MAX_EXPERTS ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
+moe_status_t check_product(moe_dtype_t dtype, moe_dtype_t w_dtype, moe_dtype_t out_dtype,
+                           const moe::GroupedGemmArgs& a, moe::GroupedProduct kind) {
+  if (a.rows < 0 || a.E < 1) return MOE_ERR_INVALID_ARG;
+  moe_status_t s = check_width(a.N);
+  if (s == MOE_OK) s = check_width(a.K);
+  if (s == MOE_OK) s = check_float_dtype(dtype);
+  if (s == MOE_OK) s = check_float_dtype(out_dtype);
+  if (s == MOE_OK && w_dtype != dtype)
+    s = w_dtype < MOE_F32 || w_dtype > MOE_FP8_E4M3FN_BLOCKED ? MOE_ERR_INVALID_ARG : MOE_ERR_UNSUPPORTED;
+  if (s != MOE_OK) return s;
+  if (a.E > MOE_MAX_EXPERTS) return MOE_ERR_UNSUPPORTED;
+  const long long R = a.rows, W = (long long)a.E * a.N * a.K;
+  const long long na = R * (kind == moe::kForward ? a.K : a.N), nb = kind == moe::kWgrad ? R * a.K : W;
+  const long long no = kind == moe::kForward ? R * a.N : (kind == moe::kDgrad ? R * a.K : W);
+  if (!ok_ptr(a.a, na, 16) || !ok_ptr(a.b, nb, 16) || !ok_ptr(a.out, no, 16) || !ok_ptr(a.offsets, a.E + 1, 4))
+    return MOE_ERR_INVALID_ARG;
+  if (R > 0 && (a.a2 == nullptr) != (a.b2 == nullptr)) return MOE_ERR_INVALID_ARG;
+  if (!aligned(a.a2, 16) || !aligned(a.b2, 16)) return MOE_ERR_INVALID_ARG;
+  return moe::grouped_gemm_fits(a, kind) ? MOE_OK : MOE_ERR_UNSUPPORTED;
+}
+
+// T, k, d and the map of the calls between tokens and sorted rows
+moe_status_t check_tokens(int T, int k, int d, const int32_t* f2s) {
+  if (T < 0 || k < 1 || k > MOE_MAX_TOPK || (long long)T * k > INT_MAX) return MOE_ERR_INVALID_ARG;
+  moe_status_t s = check_width(d);
+  if (s != MOE_OK) return s;
+  return ok_ptr(f2s, (long long)T * k, 4) ? MOE_OK : MOE_ERR_INVALID_ARG;
+}
+
 moe_status_t hip_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
 
 }  // namespace
@@ -401,6 +452,156 @@ moe_status_t moe_layer(const float* logits, const void* x, moe_dtype_t act_dtype
                           w_dtype, s_gate, s_up, s_down, topk_ids, topk_gates, counts, offsets,
                           sorted_to_flat, flat_to_sorted, x_sorted, y_sorted, y, y_dtype,
                           workspace, workspace_bytes, stream);
+}
+
+moe_status_t moe_grouped_gemm(const void* x, moe_dtype_t x_dtype, const int32_t* offsets, int rows,
+                              int E, int N, int K, const void* w, moe_dtype_t w_dtype, void* y,
+                              moe_dtype_t y_dtype, void* stream) {
+  const moe::GroupedGemmArgs a{x, w, nullptr, nullptr, y, offsets, rows, E, N, K,
+                               x_dtype == MOE_BF16, y_dtype == MOE_BF16, false};
+  moe_status_t s = check_product(x_dtype, w_dtype, y_dtype, a, moe::kForward);
+  if (s != MOE_OK || rows == 0) return s;
+  return hip_status(moe::launch_grouped_gemm(a, moe::kForward, static_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_grouped_gemm_dgrad(const void* dy, const void* dy2, moe_dtype_t dy_dtype,
+                                    const int32_t* offsets, int rows, int E, int N, int K,
+                                    const void* w, const void* w2, moe_dtype_t w_dtype, void* dx,
+                                    moe_dtype_t dx_dtype, void* stream) {
+  const moe::GroupedGemmArgs a{dy, w, dy2, w2, dx, offsets, rows, E, N, K,
+                               dy_dtype == MOE_BF16, dx_dtype == MOE_BF16, false};
+  moe_status_t s = check_product(dy_dtype, w_dtype, dx_dtype, a, moe::kDgrad);
+  if (s != MOE_OK || rows == 0) return s;
+  return hip_status(moe::launch_grouped_gemm(a, moe::kDgrad, static_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_grouped_gemm_wgrad(const void* dy, const void* x, moe_dtype_t dtype,
+                                    const int32_t* offsets, int rows, int E, int N, int K, void* dw,
+                                    moe_dtype_t dw_dtype, int accumulate, void* stream) {
+  if (accumulate != 0 && accumulate != 1) return MOE_ERR_INVALID_ARG;
+  const moe::GroupedGemmArgs a{dy, x, nullptr, nullptr, dw, offsets, rows, E, N, K,
+                               dtype == MOE_BF16, dw_dtype == MOE_BF16, accumulate == 1};
+  moe_status_t s = check_product(dtype, dtype, dw_dtype, a, moe::kWgrad);
+  if (s != MOE_OK || (rows == 0 && accumulate)) return s;
+  return hip_status(moe::launch_grouped_gemm(a, moe::kWgrad, static_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_checkpoint_pack(const void* x, moe_dtype_t x_dtype, int rows, int d, void* codes,
+                                 float* scales, void* stream) {
+  if (rows < 0) return MOE_ERR_INVALID_ARG;
+  moe_status_t s = check_width(d);
+  if (s == MOE_OK) s = check_float_dtype(x_dtype);
+  if (s != MOE_OK) return s;
+  const long long n = (long long)rows * d;
+  if (!ok_ptr(x, n, 16) || !ok_ptr(codes, n, 16) || !ok_ptr(scales, rows * held_groups(d), 4))
+    return MOE_ERR_INVALID_ARG;
+  if (moe::row_kernel_grid(rows, d) > kMaxGrid) return MOE_ERR_UNSUPPORTED;
+  return hip_status(moe::launch_pack(x, x_dtype == MOE_BF16, rows, d, codes, scales,
+                                     static_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_checkpoint_unpack(const void* codes, const float* scales, int T, int k, int d,
+                                   const int32_t* flat_to_sorted, void* out, moe_dtype_t out_dtype,
+                                   void* stream) {
+  if (T < 0 || k < 1 || k > MOE_MAX_TOPK || (long long)T * k > INT_MAX) return MOE_ERR_INVALID_ARG;
+  if (!flat_to_sorted && k != 1) return MOE_ERR_INVALID_ARG;
+  moe_status_t s = check_width(d);
+  if (s == MOE_OK) s = check_float_dtype(out_dtype);
+  if (s != MOE_OK) return s;
+  const long long n = (long long)T * d;
+  if (!ok_ptr(codes, n, 16) || !ok_ptr(scales, T * held_groups(d), 4) || !ok_ptr(out, n * k, 16) ||
+      !aligned(flat_to_sorted, 4))
+    return MOE_ERR_INVALID_ARG;
+  if (moe::row_kernel_grid(T, d) > kMaxGrid) return MOE_ERR_UNSUPPORTED;
+  return hip_status(moe::launch_unpack(codes, scales, T, k, d, flat_to_sorted, out, out_dtype == MOE_BF16,
+                                       static_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_swiglu(const void* g, const void* u, moe_dtype_t dtype, const int32_t* offsets,
+                        int E, int rows, int d_ff, void* h, void* g_codes, float* g_scales,
+                        void* u_codes, float* u_scales, void* stream) {
+  if (rows < 0) return MOE_ERR_INVALID_ARG;
+  moe_status_t s = check_width(d_ff);
+  if (s == MOE_OK) s = check_float_dtype(dtype);
+  if (s == MOE_OK) s = check_row_offsets(offsets, E);
+  if (s != MOE_OK) return s;
+  const long long n = (long long)rows * d_ff, ng = rows * held_groups(d_ff);
+  if (!ok_ptr(g, n, 16) || !ok_ptr(u, n, 16) || !ok_ptr(h, n, 16)) return MOE_ERR_INVALID_ARG;
+  if ((g_codes || g_scales || u_codes || u_scales) &&
+      (!ok_ptr(g_codes, n, 16) || !ok_ptr(u_codes, n, 16) || !ok_ptr(g_scales, ng, 4) || !ok_ptr(u_scales, ng, 4)))
+    return MOE_ERR_INVALID_ARG;
+  if (moe::row_kernel_grid(rows, d_ff) > kMaxGrid) return MOE_ERR_UNSUPPORTED;
+  return hip_status(moe::launch_swiglu(g, u, dtype == MOE_BF16, offsets, E, rows, d_ff, h, g_codes, g_scales,
+                                       u_codes, u_scales, static_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_swiglu_backward(const void* dh, moe_dtype_t dtype, const void* g, const void* u,
+                                 moe_dtype_t gu_dtype, const float* g_scales,
+                                 const float* u_scales, const int32_t* offsets, int E, int rows,
+                                 int d_ff, void* dg, void* du, void* h, void* stream) {
+  if (rows < 0) return MOE_ERR_INVALID_ARG;
+  moe_status_t s = check_width(d_ff);
+  if (s == MOE_OK) s = check_float_dtype(dtype);
+  if (s == MOE_OK) s = check_row_offsets(offsets, E);
+  if (s != MOE_OK) return s;
+  const bool held = gu_dtype == MOE_FP8_E4M3FN;
+  if (!held && gu_dtype != dtype) {
+    s = check_float_dtype(gu_dtype);
+    return s == MOE_OK ? MOE_ERR_UNSUPPORTED : s;
+  }
+  const long long n = (long long)rows * d_ff, ng = rows * held_groups(d_ff);
+  if (!ok_ptr(dh, n, 16) || !ok_ptr(g, n, 16) || !ok_ptr(u, n, 16) || !ok_ptr(dg, n, 16) || !ok_ptr(du, n, 16) ||
+      !aligned(h, 16))
+    return MOE_ERR_INVALID_ARG;
+  if (held ? (!ok_ptr(g_scales, ng, 4) || !ok_ptr(u_scales, ng, 4)) : (g_scales || u_scales))
+    return MOE_ERR_INVALID_ARG;
+  if (moe::row_kernel_grid(rows, d_ff) > kMaxGrid) return MOE_ERR_UNSUPPORTED;
+  return hip_status(moe::launch_swiglu_backward(dh, dtype == MOE_BF16, g, u, held, g_scales, u_scales, offsets,
+                                                E, rows, d_ff, dg, du, h, static_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_combine_backward(const void* dy, moe_dtype_t dy_dtype, const float* y_sorted,
+                                  const int32_t* flat_to_sorted, const float* topk_gates, int T,
+                                  int k, int d, void* dy_sorted, moe_dtype_t dys_dtype,
+                                  float* dgates, void* stream) {
+  moe_status_t s = check_tokens(T, k, d, flat_to_sorted);
+  if (s == MOE_OK) s = check_float_dtype(dy_dtype);
+  if (s == MOE_OK) s = check_float_dtype(dys_dtype);
+  if (s != MOE_OK) return s;
+  const long long R = (long long)T * k;
+  if (!ok_ptr(dy, (long long)T * d, 16) || !ok_ptr(topk_gates, R, 4) || !ok_ptr(dy_sorted, R * d, 16))
+    return MOE_ERR_INVALID_ARG;
+  if ((y_sorted || dgates) && (!ok_ptr(y_sorted, R * d, 16) || !ok_ptr(dgates, R, 4))) return MOE_ERR_INVALID_ARG;
+  if (moe::combine_backward_grid(T, k, d) > kMaxGrid) return MOE_ERR_UNSUPPORTED;
+  return hip_status(moe::launch_combine_backward(dy, dy_dtype == MOE_BF16, y_sorted, flat_to_sorted, topk_gates,
+                                                 T, k, d, dy_sorted, dys_dtype == MOE_BF16, dgates,
+                                                 static_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_permute_backward(const void* dx_sorted, moe_dtype_t dtype,
+                                  const int32_t* flat_to_sorted, int T, int k, int d, void* dx,
+                                  moe_dtype_t dx_dtype, void* stream) {
+  moe_status_t s = check_tokens(T, k, d, flat_to_sorted);
+  if (s == MOE_OK) s = check_float_dtype(dtype);
+  if (s == MOE_OK) s = check_float_dtype(dx_dtype);
+  if (s != MOE_OK) return s;
+  if (!ok_ptr(dx_sorted, (long long)T * k * d, 16) || !ok_ptr(dx, (long long)T * d, 16)) return MOE_ERR_INVALID_ARG;
+  if (moe::row_kernel_grid(T, d) > kMaxGrid) return MOE_ERR_UNSUPPORTED;
+  return hip_status(moe::launch_permute_backward(dx_sorted, dtype == MOE_BF16, flat_to_sorted, T, k, d, dx,
+                                                 dx_dtype == MOE_BF16, static_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_route_backward(const float* dgates, const int32_t* topk_ids,
+                                const float* topk_gates, int T, int E, int k, float* dlogits,
+                                void* stream) {
+  moe_status_t s = check_sizes(T, E, k);
+  if (s != MOE_OK) return s;
+  const long long R = (long long)T * k;
+  if (!ok_ptr(dgates, R, 4) || !ok_ptr(topk_ids, R, 4) || !ok_ptr(topk_gates, R, 4) ||
+      !ok_ptr(dlogits, (long long)T * E, 4))
+    return MOE_ERR_INVALID_ARG;
+  return hip_status(moe::launch_route_backward(dgates, topk_ids, topk_gates, T, E, k, dlogits,
+                                               static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

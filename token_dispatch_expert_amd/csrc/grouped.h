@@ -1,0 +1,129 @@
+// Device helpers shared by the kernels over expert-sorted rows: an expert's rows, and the tile
+// or expert that a workgroup works on, found by every wave on its own from the offsets (no LDS,
+// no barrier, one round of loads).
+#pragma once
+
+#include "moe_internal.h"
+
+namespace moe {
+
+// Rows [a, b) of expert e, with the offsets clamped into [0, rows] and made non-decreasing so
+// that corrupt offsets can never address memory out of bounds.
+__device__ __forceinline__ void group_rows(const int32_t* offsets, int e, int rows, int& a, int& b) {
+  a = offsets[e];
+  b = offsets[e + 1];
+  a = a < 0 ? 0 : (a > rows ? rows : a);
+  b = b < a ? a : (b > rows ? rows : b);
+}
+
+// Rows in use: offsets[E] when the caller gave the offsets (rows past it belong to no expert
+// and are neither read nor written), else all of them.
+__device__ __forceinline__ int rows_in_use(const int32_t* offsets, int E, int rows) {
+  if (!offsets) return rows;
+  const int n = offsets[E];
+  return n < 0 ? 0 : (n > rows ? rows : n);
+}
+
+// Workgroup b's item. The hardware deals workgroups to the 8 XCDs in turn (workgroup b runs on
+// XCD b % 8) and each XCD has an L2 of its own, so runs of kXcdRun consecutive items, which
+// share operands, go to one XCD, and the runs go round the XCDs.
+constexpr int kXcdRun = 32;
+__device__ __forceinline__ long long xcd_item(unsigned b) {
+  const unsigned x = b & 7, i = b >> 3;
+  return ((long long)(i / kXcdRun) * 8 + x) * kXcdRun + i % kXcdRun;
+}
+// Grid that covers `items` items under that map.
+inline long long xcd_grid(long long items) {
+  const long long round = 8 * kXcdRun;
+  return (items + round - 1) / round * round;
+}
+
+// Row tiles of TM rows, expert by expert; each of an expert's row tiles meets NT column tiles.
+// Finds item's expert e, its rows [a, b) and the tile pair (mt, nt) within the expert; false
+// past the last item. Within an expert, groups of kGroupM row tiles walk the column tiles
+// together, so that the tiles in flight on one XCD share both operands.
+constexpr int kGroupM = 4;
+__device__ __forceinline__ bool find_row_tile(const int32_t* offsets, int E, int rows, int TM,
+                                              int NT, long long item, int& e, int& a, int& b,
+                                              int& mt, int& nt) {
+  const int lane = threadIdx.x & 63;
+  const int per = (E + 63) / 64;  // consecutive experts per lane
+  int mine = 0;
+  for (int i = 0; i < per; ++i) {
+    const int x = lane * per + i;
+    if (x < E) {
+      int p, q;
+      group_rows(offsets, x, rows, p, q);
+      mine += (q - p + TM - 1) / TM;
+    }
+  }
+  int incl = mine;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int v = __shfl_up(incl, d);
+    if (lane >= d) incl += v;
+  }
+  const long long q64 = item / NT;
+  const int total = __shfl(incl, 63);
+  if (q64 >= total) return false;
+  const int q = (int)q64;
+  const unsigned long long past = __ballot(incl > q);  // never empty: q < total
+  const int owner = __ffsll(past) - 1;
+  int pre = __shfl(incl - mine, owner);
+  // the owner's experts, read by every lane (uniform addresses)
+  e = owner * per;
+  int mtiles = 0;
+  for (;; ++e) {
+    group_rows(offsets, e, rows, a, b);
+    mtiles = (b - a + TM - 1) / TM;
+    if (q < pre + mtiles || e + 1 >= min(E, (owner + 1) * per)) break;
+    pre += mtiles;
+  }
+  e = __builtin_amdgcn_readfirstlane(e);
+  a = __builtin_amdgcn_readfirstlane(a);
+  b = __builtin_amdgcn_readfirstlane(b);
+  pre = __builtin_amdgcn_readfirstlane(pre);
+  mtiles = __builtin_amdgcn_readfirstlane(mtiles);
+  const int local = (int)(item - (long long)pre * NT);
+  const int g = local / (kGroupM * NT);
+  const int gm = min(kGroupM, mtiles - g * kGroupM);
+  const int j = local - g * kGroupM * NT;
+  nt = j / gm;
+  mt = g * kGroupM + j % gm;
+  return true;
+}
+
+// The expert of rank r when experts are ordered by their number of rows, the most first, to
+// within a factor of two (equal powers of two keep the expert order). Work whose cost goes
+// with an expert's rows then starts with the longest.
+__device__ __forceinline__ int expert_of_rank(const int32_t* offsets, int E, int rows, int r) {
+  const int lane = threadIdx.x & 63;
+  int key[16];  // E <= MOE_MAX_EXPERTS = 1024
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    key[i] = -1;
+    const int x = lane + 64 * i;
+    if (64 * i < E && x < E) {
+      int a, b;
+      group_rows(offsets, x, rows, a, b);
+      key[i] = 32 - __clz(b - a);
+    }
+  }
+  int before = 0;
+  for (int k = 31; k >= 0; --k) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if (64 * i >= E) break;
+      unsigned long long m = __ballot(key[i] == k);
+      const int n = __popcll(m);
+      if (r < before + n) {
+        for (int s = r - before; s > 0; --s) m &= m - 1;
+        return __builtin_amdgcn_readfirstlane(64 * i + __ffsll(m) - 1);
+      }
+      before += n;
+    }
+  }
+  return 0;  // not reached for r < E
+}
+
+}  // namespace moe

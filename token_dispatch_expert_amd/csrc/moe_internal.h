@@ -13,6 +13,7 @@ namespace moe {
 // vector types used for MFMA operands and 16-byte memory moves
 // ---------------------------------------------------------------------------------------
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
@@ -104,6 +105,47 @@ hipError_t launch_grouped_ffn(const FfnArgs& a, const DeviceInfo& dev, hipStream
 hipError_t launch_combine(const float* y_sorted, const int32_t* flat_to_sorted,
                           const float* gates, int T, int k, int d, void* y, bool bf16_out,
                           hipStream_t stream);
+
+// Matrix products grouped by expert (grouped_gemm.hip). Operands in bf16 or fp32; W [E, N, K].
+//   forward  a = x [rows, K],  b = W,              out [rows, N]
+//   dgrad    a = dy [rows, N], b = W (a2, b2: a second pair or null), out [rows, K]
+//   wgrad    a = dy [rows, N], b = x [rows, K],    out [E, N, K]
+struct GroupedGemmArgs {
+  const void *a, *b, *a2, *b2;
+  void* out;
+  const int32_t* offsets;
+  int rows, E, N, K;
+  bool bf16, out_bf16, accumulate;
+};
+enum GroupedProduct : int { kForward = 0, kDgrad = 1, kWgrad = 2 };
+// whether the product's tiles fit one launch's grid
+bool grouped_gemm_fits(const GroupedGemmArgs& a, GroupedProduct kind);
+hipError_t launch_grouped_gemm(const GroupedGemmArgs& a, GroupedProduct kind, hipStream_t stream);
+
+// Row-wise kernels of the training step (checkpoint.hip, backward.hip); d, f multiples of 8.
+long long row_kernel_grid(long long rows, int d);  // workgroups (to check against the grid limit)
+hipError_t launch_pack(const void* x, bool bf16, int rows, int d, void* codes, float* scales,
+                       hipStream_t stream);
+// f2s [T, k] (the row of each of token t's assignments) or null: out row t
+hipError_t launch_unpack(const void* codes, const float* scales, int T, int k, int d,
+                         const int32_t* f2s, void* out, bool bf16, hipStream_t stream);
+// offsets [E + 1] or null: only the first offsets[E] rows; codes and scales all null: h alone
+hipError_t launch_swiglu(const void* g, const void* u, bool bf16, const int32_t* offsets, int E,
+                         int rows, int f, void* h, void* g_codes, float* g_scales, void* u_codes,
+                         float* u_scales, hipStream_t stream);
+hipError_t launch_swiglu_backward(const void* dh, bool bf16, const void* g, const void* u, bool held,
+                                  const float* g_scales, const float* u_scales,
+                                  const int32_t* offsets, int E, int rows, int f, void* dg, void* du,
+                                  void* h, hipStream_t stream);
+long long combine_backward_grid(int T, int k, int d);
+hipError_t launch_combine_backward(const void* dy, bool dy_bf16, const float* y_sorted,
+                                   const int32_t* flat_to_sorted, const float* gates, int T, int k,
+                                   int d, void* dy_sorted, bool out_bf16, float* dgates,
+                                   hipStream_t stream);
+hipError_t launch_permute_backward(const void* dx_sorted, bool bf16, const int32_t* flat_to_sorted,
+                                   int T, int k, int d, void* dx, bool out_bf16, hipStream_t stream);
+hipError_t launch_route_backward(const float* dgates, const int32_t* ids, const float* gates, int T,
+                                 int E, int k, float* dlogits, hipStream_t stream);
 
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
