@@ -64,18 +64,18 @@ __device__ __forceinline__ bool find_row_tile(const int32_t* offsets, int E, int
     if (lane >= d) incl += v;
   }
   const long long q64 = item / NT;
-  const int total = __shfl(incl, 63);
+  const int total = __builtin_amdgcn_readlane(incl, 63);
   if (q64 >= total) return false;
   const int q = (int)q64;
   const unsigned long long past = __ballot(incl > q);  // never empty: q < total
   const int owner = __ffsll(past) - 1;
-  int pre = __shfl(incl - mine, owner);
+  int pre = __builtin_amdgcn_readlane(incl - mine, owner);
   // the owner's experts, read by every lane (uniform addresses)
   e = owner * per;
   int mtiles = 0;
   for (;; ++e) {
     group_rows(offsets, e, rows, a, b);
-    mtiles = (b - a + TM - 1) / TM;
+    mtiles = __builtin_amdgcn_readfirstlane((b - a + TM - 1) / TM);
     if (q < pre + mtiles || e + 1 >= min(E, (owner + 1) * per)) break;
     pre += mtiles;
   }

@@ -14,6 +14,7 @@
 //   dgrad    A = dy along N,  B = W across N
 //   wgrad    A = dy across r, B = x across r
 #include "grouped.h"
+#include "lds_tiles.h"
 
 namespace moe {
 
@@ -32,6 +33,7 @@ namespace {
 // C: one 16-byte (fp32) or 8-byte (bf16) store.
 constexpr int kStep = 32;
 constexpr int kPad = 4;
+constexpr int kF32Tile = 64;
 
 template <typename T> struct Chunk;  // 4 elements as stored
 template <> struct Chunk<float> { float4 v; };
@@ -66,6 +68,39 @@ __device__ __forceinline__ void store4(const ProductArgs& p, size_t at, f32x4 v)
     if (p.accumulate) v += *o;
     *o = v;
   }
+}
+
+// Where a tile lies: expert, its rows [ra, rb), C's rows from m0 (of mlim in the tile) and
+// columns from c0 (of clim), and the contraction's length.
+struct TileAt {
+  int e, ra, rb, m0, mlim, c0, clim, kdim;
+};
+template <GroupedProduct P>
+__device__ __forceinline__ bool tile_at(const ProductArgs& p, int TM, int TN, TileAt& t) {
+  const long long item = xcd_item(blockIdx.x);
+  const int cols = P == kForward ? p.N : p.K;
+  const int CT = (cols + TN - 1) / TN;
+  int mt, nt;
+  if constexpr (P == kWgrad) {
+    const long long per = (long long)((p.N + TM - 1) / TM) * CT;
+    if (item >= p.E * per) return false;
+    const int local = (int)(item % per);
+    t.e = expert_of_rank(p.offsets, p.E, p.rows, (int)(item / per));
+    group_rows(p.offsets, t.e, p.rows, t.ra, t.rb);
+    mt = local / CT;
+    nt = local % CT;
+    if (t.ra == t.rb && p.accumulate) return false;
+  } else {
+    if (!find_row_tile(p.offsets, p.E, p.rows, TM, CT, item, t.e, t.ra, t.rb, mt, nt)) return false;
+  }
+  t.m0 = mt * TM;
+  t.c0 = nt * TN;
+  t.mlim = min(TM, (P == kWgrad ? p.N : t.rb - t.ra) - t.m0);
+  t.clim = min(TN, cols - t.c0);
+  t.kdim = P == kForward ? p.K : (P == kDgrad ? p.N : t.rb - t.ra);
+  // the same in every lane: kept in scalar registers, as buffer descriptors need it
+  for (int* v : {&t.e, &t.ra, &t.rb, &t.m0, &t.mlim, &t.c0, &t.clim, &t.kdim}) *v = __builtin_amdgcn_readfirstlane(*v);
+  return true;
 }
 
 // One operand of one step: TM rows (along) or columns (across) of C's side, 32 of the
@@ -123,29 +158,13 @@ __global__ __launch_bounds__(256) void product_kernel(ProductArgs p) {
   constexpr int FR = TM / 32;  // 16-wide fragments per wave and side
   __shared__ __align__(16) float la[stage_floats<AX, TM>()];
   __shared__ __align__(16) float lb[stage_floats<BX, TM>()];
-  const long long item = xcd_item(blockIdx.x);
+  TileAt t;
+  if (!tile_at<P>(p, TM, TM, t)) return;
+  const int e = t.e, ra = t.ra, m0 = t.m0, c0 = t.c0, mlim = t.mlim, clim = t.clim, kdim = t.kdim;
+  const int cols = P == kForward ? p.N : p.K;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave & 1, wn = wave >> 1;
-  const int cols = P == kForward ? p.N : p.K;
-  const int CT = (cols + TM - 1) / TM;
-  int e, ra, rb, mt, nt;
-  if constexpr (P == kWgrad) {
-    const int MT = (p.N + TM - 1) / TM;
-    if (item >= (long long)p.E * MT * CT) return;
-    const int local = (int)(item % ((long long)MT * CT));
-    e = expert_of_rank(p.offsets, p.E, p.rows, (int)(item / ((long long)MT * CT)));
-    group_rows(p.offsets, e, p.rows, ra, rb);
-    mt = local / CT;
-    nt = local % CT;
-    if (ra == rb && p.accumulate) return;
-  } else {
-    if (!find_row_tile(p.offsets, p.E, p.rows, TM, CT, item, e, ra, rb, mt, nt)) return;
-  }
-  // C's rows and columns of the tile
-  const int m0 = mt * TM, c0 = nt * TM;
-  const int mlim = min(TM, (P == kWgrad ? p.N : rb - ra) - m0), clim = min(TM, cols - c0);
-  const int kdim = P == kForward ? p.K : (P == kDgrad ? p.N : rb - ra);
   const int lda = P == kForward ? p.K : p.N;
   const size_t wbase = (size_t)e * p.N * p.K;
   const size_t a_at = P == kWgrad ? (size_t)ra * p.N + m0 : (size_t)(ra + m0) * lda;
@@ -205,19 +224,248 @@ __global__ __launch_bounds__(256) void product_kernel(ProductArgs p) {
   }
 }
 
-// Tiles that a launch covers: for wgrad every expert's, for the row products the most that the
-// rows can fill (an expert's last row tile may be partial).
-long long tile_items(GroupedProduct kind, const GroupedGemmArgs& a, int TM) {
-  const long long nt = (a.N + TM - 1) / TM, kt = (a.K + TM - 1) / TM;
-  if (kind == kWgrad) return a.E * nt * kt;
-  const long long mt = a.rows / TM + (a.E < a.rows ? a.E : a.rows);
-  return mt * (kind == kForward ? nt : kt);
+// ---------------------------------------------------------------------------------------
+// bf16: tiles loaded straight into LDS
+// ---------------------------------------------------------------------------------------
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+// One transposing LDS read. The pointer is declared not to alias anything so that the compiler
+// does not take the read to depend on the loads into LDS that are in flight (it would wait for
+// all of them first, in every step); what is read has landed, the kernel's own waits see to that.
+__device__ __forceinline__ s16x4 read_transposed(const char* __restrict__ at) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)at);
 }
 
-template <typename T, GroupedProduct P, int TM>
+// One operand of a tile: T rows or columns of C's side, DK of the contraction per step, loaded
+// by NW waves with buffer loads of 1 KB into LDS (16 bytes a lane). The LDS image is the
+// operand's memory order, [T][DK] (along) or [DK][T] (across), in 16-byte chunks that are
+// permuted within a row so that the lanes of a fragment read fall on distinct banks:
+//   along   dswz of lds_tiles.h; a fragment is one 16-byte read, 8 contraction elements of row
+//           lane % 16, chunk lane / 16
+//   across  32-byte units, unit u of row k at u ^ x(k), x(k) = (k & 3) + 4 ((k >> 3) & 1); a fragment
+//           is two transposing reads, each 4 contraction rows of 16 columns per 16 lanes (lane i
+//           gives the address of row i / 4, columns 4 (i % 4) .. + 3, and gets column i of the 4
+//           rows). The units of the 8 rows that a read of 32 lanes touches differ.
+// Lane group g = lane / 16 takes contraction elements 8g .. 8g + 7 of a 32-long slice in both
+// forms, so along and across operands meet.
+template <bool ACROSS, int T, int DK, int NW>
+struct Operand {
+  static constexpr int kChunks = T * DK / 8;          // 16-byte chunks per step
+  static constexpr int kRowChunks = (ACROSS ? T : DK) / 8;
+  static constexpr int kLoads = kChunks / 64 / NW;    // load instructions per wave and step
+  static constexpr int kRowsPerLoad = 64 / kRowChunks;
+  static_assert(kLoads >= 1 && kLoads * 64 * NW == kChunks, "loads split evenly over the waves");
+  static_assert(!ACROSS || T >= 128, "across: at least 8 units in a row");
+  static_assert(kRowsPerLoad * NW % 16 == 0, "the permutation repeats from one load to the next");
+  // Past any extent (at most 2^20 * 2 * 256 bytes): the lanes that load nothing but zeros.
+  static constexpr int kOutside = 0x40000000;
+
+  const char* base;  // along: the tile's first row; across: its first column in row 0
+  unsigned extent;   // along: bytes of the tile's rows
+  int ld;            // row stride in bytes
+  int col;           // across: bytes before the tile's first column in a row
+  int lane_at, stride, k_of_lane;
+
+  __device__ __forceinline__ static int unit(int k) { return (k & 3) | ((k >> 3) & 1) << 2; }
+
+  // origin: the operand's element (0, 0) for this expert; first: the tile's first row (along)
+  // or column (across); count: how many rows of the tile exist (along); ld_elems: row stride.
+  __device__ __forceinline__ void set(const __bf16* origin, int first, int count, int ld_elems, int wave, int lane) {
+    ld = ld_elems * 2;
+    const int row = wave * kRowsPerLoad + lane / kRowChunks, pos = lane % kRowChunks;
+    stride = NW * kRowsPerLoad * ld;
+    if constexpr (ACROSS) {
+      base = reinterpret_cast<const char*>(origin) + (size_t)first * 2;
+      col = first * 2;
+      lane_at = row * ld + (pos ^ (unit(row) << 1)) * 16;
+    } else {
+      base = reinterpret_cast<const char*>(origin) + (size_t)first * ld;
+      extent = (unsigned)count * (unsigned)ld;
+      const int chunk = dswz<kRowChunks>(row, pos) - row * kRowChunks;
+      lane_at = row * ld + chunk * 16;
+      k_of_lane = chunk * 8;
+    }
+  }
+
+  // Contraction elements k0 .. k0 + DK - 1 of the tile into `slot`; those at or past kdim, and
+  // rows or columns that do not exist, become zeros. `moved`: bytes from this operand to the one
+  // of the second pair.
+  template <int AUX>
+  __device__ __forceinline__ void issue(u32x4* slot, int k0, int kdim, ptrdiff_t moved, int wave) const {
+    if constexpr (ACROSS) {
+      const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+          (void*)(base + moved + (size_t)k0 * ld), (short)0, min(DK, kdim - k0) * ld - col, kBufferWord3);
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i)
+        buffer_load_lds16<AUX>(r, slot + (wave + i * NW) * 64, lane_at + i * stride, 0);
+    } else {
+      const __amdgpu_buffer_rsrc_t r =
+          __builtin_amdgcn_make_buffer_rsrc((void*)(base + moved), (short)0, (int)extent, kBufferWord3);
+      const bool in = k_of_lane < kdim - k0;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i)
+        buffer_load_lds16<AUX>(r, slot + (wave + i * NW) * 64, in ? lane_at + i * stride : kOutside, k0 * 2);
+    }
+  }
+
+  // Fragment of 16 rows or columns from m0, contraction slice h (32 elements).
+  __device__ __forceinline__ static bf16x8 read(const u32x4* slot, int m0, int h, int lane) {
+    bf16x8 f;
+    if constexpr (ACROSS) {
+      const int i = lane & 15, g = lane >> 4;
+      const int k = h * 32 + g * 8 + (i >> 2);
+      const char* at = reinterpret_cast<const char*>(slot) + k * (T * 2) + ((m0 >> 4) ^ unit(k)) * 32 + (i & 3) * 8;
+      const s16x4 v[2] = {read_transposed(at), read_transposed(at + 4 * T * 2)};  // unit(k + 4) = unit(k)
+      __builtin_memcpy(&f, v, 16);
+    } else {
+      const u32x4 v = slot[dswz<kRowChunks>(m0 + (lane & 15), h * 4 + (lane >> 4))];
+      __builtin_memcpy(&f, &v, 16);
+    }
+    return f;
+  }
+};
+
+// Workgroup barrier without a fence: a fence would make the compiler wait for every outstanding
+// load into LDS. The signal fences keep the compiler from moving LDS accesses across it.
+__device__ __forceinline__ void bare_barrier() {
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  __builtin_amdgcn_s_barrier();
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+}
+
+// A workgroup of WGM x WGN waves computes a tile of C, each wave WM x WN of it with
+// v_mfma_f32_16x16x32_bf16; steps of DK go through a ring of RING slots in LDS. While a
+// slice's products run, the fragments of the next slice are read (B into the other of two
+// register sets, each A fragment after its last product); the barrier that frees a step's slot
+// stands before the products of the step's last slice, whose fragments are in registers by then.
+template <GroupedProduct P, int WM, int WN, int WGM, int WGN, int DK, int RING, bool ONCE>
+__global__ __launch_bounds__(64 * WGM * WGN) void tile_kernel(ProductArgs p) {
+  constexpr bool AX = P == kWgrad, BX = P != kForward;
+  constexpr int TM = WM * WGM, TN = WN * WGN, NW = WGM * WGN;
+  constexpr int MF = WM / 16, NF = WN / 16, NS = DK / 32;
+  using OA = Operand<AX, TM, DK, NW>;
+  using OB = Operand<BX, TN, DK, NW>;
+  constexpr int STAGE = OA::kChunks + OB::kChunks, LOADS = OA::kLoads + OB::kLoads;
+  __shared__ __align__(16) u32x4 ring[RING * STAGE];
+  TileAt t;
+  if (!tile_at<P>(p, TM, TN, t)) return;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / WGN * WM, wn = wave % WGN * WN;
+
+  OA oa;
+  OB ob;
+  const size_t weights = (size_t)t.e * p.N * p.K;
+  const __bf16 *a = static_cast<const __bf16*>(p.a), *b = static_cast<const __bf16*>(p.b);
+  if constexpr (P == kForward) {
+    oa.set(a + (size_t)t.ra * p.K, t.m0, t.mlim, p.K, wave, lane);
+    ob.set(b + weights, t.c0, t.clim, p.K, wave, lane);
+  } else if constexpr (P == kDgrad) {
+    oa.set(a + (size_t)t.ra * p.N, t.m0, t.mlim, p.N, wave, lane);
+    ob.set(b + weights, t.c0, t.clim, p.K, wave, lane);
+  } else {
+    oa.set(a + (size_t)t.ra * p.N, t.m0, t.mlim, p.N, wave, lane);
+    ob.set(b + (size_t)t.ra * p.K, t.c0, t.clim, p.K, wave, lane);
+  }
+  const bool pair = P == kDgrad && p.a2;
+  const ptrdiff_t moved_a = pair ? static_cast<const char*>(p.a2) - static_cast<const char*>(p.a) : 0;
+  const ptrdiff_t moved_b = pair ? static_cast<const char*>(p.b2) - static_cast<const char*>(p.b) : 0;
+  const int steps1 = (t.kdim + DK - 1) / DK, steps = pair ? 2 * steps1 : steps1;
+  const bool once = ONCE && t.rb - t.ra <= TM;  // the expert's weights are read by this row tile alone
+
+  auto issue = [&](int st) __attribute__((always_inline)) {
+    u32x4* slot = ring + st % RING * STAGE;
+    const bool second = st >= steps1;
+    const int k0 = (second ? st - steps1 : st) * DK;
+    oa.template issue<0>(slot, k0, t.kdim, second ? moved_a : 0, wave);
+    if (once)
+      ob.template issue<kNonTemporal>(slot + OA::kChunks, k0, t.kdim, second ? moved_b : 0, wave);
+    else
+      ob.template issue<0>(slot + OA::kChunks, k0, t.kdim, second ? moved_b : 0, wave);
+  };
+
+  f32x4 acc[MF][NF];
+#pragma unroll
+  for (int i = 0; i < MF; ++i)
+#pragma unroll
+    for (int j = 0; j < NF; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  if (steps > 0) {
+    bf16x8 fa[MF], fb[2][NF];
+#pragma unroll
+    for (int r = 0; r < RING; ++r)
+      if (r < steps) issue(r);
+    wait_vmcnt_dyn<(RING - 1) * LOADS>(min(RING - 1, steps - 1) * LOADS);
+    bare_barrier();
+#pragma unroll
+    for (int j = 0; j < NF; ++j) fb[0][j] = OB::read(ring + OA::kChunks, wn + j * 16, 0, lane);
+#pragma unroll
+    for (int i = 0; i < MF; ++i) fa[i] = OA::read(ring, wm + i * 16, 0, lane);
+    for (int st = 0; st < steps; ++st) {
+      const u32x4* slot = ring + st % RING * STAGE;
+      const u32x4* next = ring + (st + 1) % RING * STAGE;
+      static_for<NS>([&](auto hc) __attribute__((always_inline)) {
+        constexpr int h = decltype(hc)::value, cur = h & 1;
+        if (h == NS - 1) {
+          wait_lgkmcnt0();  // this wave's reads of step st are back
+          if (st + 1 < steps) {
+            // step st + 1 has landed for this wave, and after the barrier for all; all are done
+            // with step st's slot
+            wait_vmcnt_dyn<(RING - 2) * LOADS>(min(RING - 2, steps - 2 - st) * LOADS);
+            bare_barrier();
+            if (st + RING < steps) issue(st + RING);
+          }
+        }
+        // Past the last step these reads bring nothing that is used (any slot, in bounds).
+        const u32x4* rs = h + 1 < NS ? slot : next;
+        constexpr int rh = (h + 1) % NS;
+#pragma unroll
+        for (int j = 0; j < NF; ++j) fb[cur ^ 1][j] = OB::read(rs + OA::kChunks, wn + j * 16, rh, lane);
+#pragma unroll
+        for (int i = 0; i < MF; ++i) {
+#pragma unroll
+          for (int j = 0; j < NF; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[cur][j], fa[i], acc[i][j], 0, 0, 0);
+          fa[i] = OA::read(rs, wm + i * 16, rh, lane);
+        }
+        // order of the slice: the B reads, then each A fragment's products and its next read
+        __builtin_amdgcn_sched_group_barrier(0x100, NF * (BX ? 2 : 1), 0);
+#pragma unroll
+        for (int i = 0; i < MF; ++i) {
+          __builtin_amdgcn_sched_group_barrier(0x008, NF, 0);
+          __builtin_amdgcn_sched_group_barrier(0x100, AX ? 2 : 1, 0);
+        }
+        __atomic_signal_fence(__ATOMIC_SEQ_CST);  // the reads stay in this slice
+      });
+    }
+  }
+  // each lane holds 4 consecutive columns (from 4 (lane / 16)) of row lane % 16 of a fragment
+  const int cols = P == kForward ? p.N : p.K;
+  const size_t row0 = P == kWgrad ? (size_t)t.e * p.N + t.m0 : (size_t)t.ra + t.m0;
+#pragma unroll
+  for (int i = 0; i < MF; ++i) {
+    const int r = wm + i * 16 + (lane & 15);
+    if (r >= t.mlim) continue;
+#pragma unroll
+    for (int j = 0; j < NF; ++j) {
+      const int c = wn + j * 16 + (lane >> 4) * 4;
+      if (c < t.clim) store4(p, (row0 + r) * cols + t.c0 + c, acc[i][j]);
+    }
+  }
+}
+
+// Tiles of TM x TN that a launch covers: for wgrad every expert's, for the row products the
+// most that the rows can fill (an expert's last row tile may be partial).
+long long tile_items(GroupedProduct kind, const GroupedGemmArgs& a, int TM, int TN) {
+  const long long cols = ((kind == kForward ? a.N : a.K) + TN - 1LL) / TN;
+  if (kind == kWgrad) return a.E * ((a.N + TM - 1LL) / TM) * cols;
+  return (a.rows / TM + (a.E < a.rows ? a.E : a.rows)) * cols;
+}
+
+template <GroupedProduct P, int WM, int WN, int WGM, int WGN, int DK, int RING, bool ONCE>
 hipError_t launch_tiles(const GroupedGemmArgs& a, const ProductArgs& p, hipStream_t stream) {
-  const long long grid = xcd_grid(tile_items(P, a, TM));
-  product_kernel<T, P, TM><<<(unsigned)grid, 256, 0, stream>>>(p);
+  const long long grid = xcd_grid(tile_items(P, a, WM * WGM, WN * WGN));
+  tile_kernel<P, WM, WN, WGM, WGN, DK, RING, ONCE><<<(unsigned)grid, 64 * WGM * WGN, 0, stream>>>(p);
   return hipGetLastError();
 }
 
@@ -225,13 +473,27 @@ template <GroupedProduct P>
 hipError_t launch_product(const GroupedGemmArgs& a, hipStream_t stream) {
   const ProductArgs p{a.a, a.b, a.a2, a.b2, a.out, a.offsets, a.rows, a.E, a.N, a.K,
                       a.out_bf16 ? 1 : 0, a.accumulate ? 1 : 0};
-  return a.bf16 ? launch_tiles<__bf16, P, 64>(a, p, stream) : launch_tiles<float, P, 64>(a, p, stream);
+  if (!a.bf16) {
+    const long long grid = xcd_grid(tile_items(P, a, kF32Tile, kF32Tile));
+    product_kernel<float, P, kF32Tile><<<(unsigned)grid, 256, 0, stream>>>(p);
+    return hipGetLastError();
+  }
+  const long long mean = a.rows / a.E;  // rows per expert
+  if constexpr (P == kWgrad) {
+    if (mean >= 128 && a.N > 128 && a.K > 128) return launch_tiles<P, 128, 64, 2, 4, 64, 2, false>(a, p, stream);
+    return launch_tiles<P, 64, 64, 2, 2, 64, 2, false>(a, p, stream);
+  } else {
+    if (mean >= 128) return launch_tiles<P, 128, 64, 2, 4, 64, 2, false>(a, p, stream);
+    if (mean >= 32) return launch_tiles<P, 64, 64, 2, 2, 64, 2, false>(a, p, stream);
+    if constexpr (P == kForward) return launch_tiles<P, 32, 16, 1, 4, 128, 4, true>(a, p, stream);
+    return launch_tiles<P, 32, 32, 1, 4, 64, 4, true>(a, p, stream);
+  }
 }
 
 }  // namespace
 
 bool grouped_gemm_fits(const GroupedGemmArgs& a, GroupedProduct kind) {
-  return xcd_grid(tile_items(kind, a, 64)) <= 0x7fffffffLL;
+  return xcd_grid(tile_items(kind, a, 32, 64)) <= 0x7fffffffLL;  // the smallest tiles
 }
 
 hipError_t launch_grouped_gemm(const GroupedGemmArgs& a, GroupedProduct kind, hipStream_t stream) {
