@@ -38,11 +38,20 @@ inline long long xcd_grid(long long items) {
   return (items + round - 1) / round * round;
 }
 
-// Row tiles of TM rows, expert by expert; each of an expert's row tiles meets NT column tiles.
-// Finds item's expert e, its rows [a, b) and the tile pair (mt, nt) within the expert; false
-// past the last item. Within an expert, groups of kGroupM row tiles walk the column tiles
+// Tile pair of the i-th of mtiles * NT tiles: groups of kGroupM row tiles walk the column tiles
 // together, so that the tiles in flight on one XCD share both operands.
 constexpr int kGroupM = 4;
+__device__ __forceinline__ void tile_pair(int i, int mtiles, int NT, int& mt, int& nt) {
+  const int g = i / (kGroupM * NT);
+  const int gm = min(kGroupM, mtiles - g * kGroupM);
+  const int j = i - g * kGroupM * NT;
+  nt = j / gm;
+  mt = g * kGroupM + j % gm;
+}
+
+// Row tiles of TM rows, expert by expert; each of an expert's row tiles meets NT column tiles.
+// Finds item's expert e, its rows [a, b) and the tile pair (mt, nt) within the expert; false
+// past the last item.
 __device__ __forceinline__ bool find_row_tile(const int32_t* offsets, int E, int rows, int TM,
                                               int NT, long long item, int& e, int& a, int& b,
                                               int& mt, int& nt) {
@@ -84,12 +93,7 @@ __device__ __forceinline__ bool find_row_tile(const int32_t* offsets, int E, int
   b = __builtin_amdgcn_readfirstlane(b);
   pre = __builtin_amdgcn_readfirstlane(pre);
   mtiles = __builtin_amdgcn_readfirstlane(mtiles);
-  const int local = (int)(item - (long long)pre * NT);
-  const int g = local / (kGroupM * NT);
-  const int gm = min(kGroupM, mtiles - g * kGroupM);
-  const int j = local - g * kGroupM * NT;
-  nt = j / gm;
-  mt = g * kGroupM + j % gm;
+  tile_pair((int)(item - (long long)pre * NT), mtiles, NT, mt, nt);
   return true;
 }
 

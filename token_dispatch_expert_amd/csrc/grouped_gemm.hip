@@ -75,7 +75,10 @@ __device__ __forceinline__ void store4(const ProductArgs& p, size_t at, f32x4 v)
 struct TileAt {
   int e, ra, rb, m0, mlim, c0, clim, kdim;
 };
-template <GroupedProduct P>
+// DEAL: C's rows are dealt to their row tiles in 16-row fragments as evenly as the number of
+// tiles allows (300 rows: tiles of 160 and 140, not 256 and 44), so that row tiles side by side,
+// which read the same B, take about the same time.
+template <GroupedProduct P, bool DEAL>
 __device__ __forceinline__ bool tile_at(const ProductArgs& p, int TM, int TN, TileAt& t) {
   const long long item = xcd_item(blockIdx.x);
   const int cols = P == kForward ? p.N : p.K;
@@ -87,15 +90,21 @@ __device__ __forceinline__ bool tile_at(const ProductArgs& p, int TM, int TN, Ti
     const int local = (int)(item % per);
     t.e = expert_of_rank(p.offsets, p.E, p.rows, (int)(item / per));
     group_rows(p.offsets, t.e, p.rows, t.ra, t.rb);
-    mt = local / CT;
-    nt = local % CT;
+    tile_pair(local, (p.N + TM - 1) / TM, CT, mt, nt);
     if (t.ra == t.rb && p.accumulate) return false;
   } else {
     if (!find_row_tile(p.offsets, p.E, p.rows, TM, CT, item, t.e, t.ra, t.rb, mt, nt)) return false;
   }
+  const int n = P == kWgrad ? p.N : t.rb - t.ra;  // C's rows
   t.m0 = mt * TM;
+  t.mlim = min(TM, n - t.m0);
+  if constexpr (DEAL) {
+    const int tiles = (n + TM - 1) / TM, frags = (n + 15) / 16;
+    const int q = frags / tiles, more = frags - q * tiles;  // the first `more` tiles take q + 1
+    t.m0 = 16 * (mt * q + min(mt, more));
+    t.mlim = min(16 * (q + (mt < more ? 1 : 0)), n - t.m0);
+  }
   t.c0 = nt * TN;
-  t.mlim = min(TM, (P == kWgrad ? p.N : t.rb - t.ra) - t.m0);
   t.clim = min(TN, cols - t.c0);
   t.kdim = P == kForward ? p.K : (P == kDgrad ? p.N : t.rb - t.ra);
   // the same in every lane: kept in scalar registers, as buffer descriptors need it
@@ -159,7 +168,7 @@ __global__ __launch_bounds__(256) void product_kernel(ProductArgs p) {
   __shared__ __align__(16) float la[stage_floats<AX, TM>()];
   __shared__ __align__(16) float lb[stage_floats<BX, TM>()];
   TileAt t;
-  if (!tile_at<P>(p, TM, TM, t)) return;
+  if (!tile_at<P, false>(p, TM, TM, t)) return;
   const int e = t.e, ra = t.ra, m0 = t.m0, c0 = t.c0, mlim = t.mlim, clim = t.clim, kdim = t.kdim;
   const int cols = P == kForward ? p.N : p.K;
   const int lane = threadIdx.x & 63;
@@ -338,7 +347,10 @@ __device__ __forceinline__ void bare_barrier() {
 // slice's products run, the fragments of the next slice are read (B into the other of two
 // register sets, each A fragment after its last product); the barrier that frees a step's slot
 // stands before the products of the step's last slice, whose fragments are in registers by then.
-template <GroupedProduct P, int WM, int WN, int WGM, int WGN, int DK, int RING, bool ONCE>
+// DEAL: each wave runs a loop compiled for the number of its 16-row fragments that hold rows, so
+// a partial tile costs what its rows need; waves w and w + 4 share a SIMD and own different
+// halves of the tile, so every SIMD has work.
+template <GroupedProduct P, int WM, int WN, int WGM, int WGN, int DK, int RING, bool ONCE, bool DEAL>
 __global__ __launch_bounds__(64 * WGM * WGN) void tile_kernel(ProductArgs p) {
   constexpr bool AX = P == kWgrad, BX = P != kForward;
   constexpr int TM = WM * WGM, TN = WN * WGN, NW = WGM * WGN;
@@ -348,7 +360,7 @@ __global__ __launch_bounds__(64 * WGM * WGN) void tile_kernel(ProductArgs p) {
   constexpr int STAGE = OA::kChunks + OB::kChunks, LOADS = OA::kLoads + OB::kLoads;
   __shared__ __align__(16) u32x4 ring[RING * STAGE];
   TileAt t;
-  if (!tile_at<P>(p, TM, TN, t)) return;
+  if (!tile_at<P, DEAL>(p, TM, TN, t)) return;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WGN * WM, wn = wave % WGN * WN;
@@ -384,23 +396,28 @@ __global__ __launch_bounds__(64 * WGM * WGN) void tile_kernel(ProductArgs p) {
       ob.template issue<0>(slot + OA::kChunks, k0, t.kdim, second ? moved_b : 0, wave);
   };
 
-  f32x4 acc[MF][NF];
+  const int cols = P == kForward ? p.N : p.K;
+  const size_t row0 = P == kWgrad ? (size_t)t.e * p.N + t.m0 : (size_t)t.ra + t.m0;
+  // F: this wave's fragments with rows
+  auto run = [&](auto present) __attribute__((always_inline)) {
+    constexpr int F = decltype(present)::value;
+    f32x4 acc[F ? F : 1][NF];
 #pragma unroll
-  for (int i = 0; i < MF; ++i)
+    for (int i = 0; i < F; ++i)
 #pragma unroll
-    for (int j = 0; j < NF; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-  if (steps > 0) {
-    bf16x8 fa[MF], fb[2][NF];
+      for (int j = 0; j < NF; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    bf16x8 fa[F ? F : 1], fb[2][NF];
+    if (steps > 0) {
 #pragma unroll
-    for (int r = 0; r < RING; ++r)
-      if (r < steps) issue(r);
-    wait_vmcnt_dyn<(RING - 1) * LOADS>(min(RING - 1, steps - 1) * LOADS);
-    bare_barrier();
+      for (int r = 0; r < RING; ++r)
+        if (r < steps) issue(r);
+      wait_vmcnt_dyn<(RING - 1) * LOADS>(min(RING - 1, steps - 1) * LOADS);
+      bare_barrier();
 #pragma unroll
-    for (int j = 0; j < NF; ++j) fb[0][j] = OB::read(ring + OA::kChunks, wn + j * 16, 0, lane);
+      for (int j = 0; j < (F ? NF : 0); ++j) fb[0][j] = OB::read(ring + OA::kChunks, wn + j * 16, 0, lane);
 #pragma unroll
-    for (int i = 0; i < MF; ++i) fa[i] = OA::read(ring, wm + i * 16, 0, lane);
+      for (int i = 0; i < F; ++i) fa[i] = OA::read(ring, wm + i * 16, 0, lane);
+    }
     for (int st = 0; st < steps; ++st) {
       const u32x4* slot = ring + st % RING * STAGE;
       const u32x4* next = ring + (st + 1) % RING * STAGE;
@@ -420,37 +437,43 @@ __global__ __launch_bounds__(64 * WGM * WGN) void tile_kernel(ProductArgs p) {
         const u32x4* rs = h + 1 < NS ? slot : next;
         constexpr int rh = (h + 1) % NS;
 #pragma unroll
-        for (int j = 0; j < NF; ++j) fb[cur ^ 1][j] = OB::read(rs + OA::kChunks, wn + j * 16, rh, lane);
+        for (int j = 0; j < (F ? NF : 0); ++j) fb[cur ^ 1][j] = OB::read(rs + OA::kChunks, wn + j * 16, rh, lane);
 #pragma unroll
-        for (int i = 0; i < MF; ++i) {
+        for (int i = 0; i < F; ++i) {
 #pragma unroll
           for (int j = 0; j < NF; ++j)
             acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[cur][j], fa[i], acc[i][j], 0, 0, 0);
           fa[i] = OA::read(rs, wm + i * 16, rh, lane);
         }
         // order of the slice: the B reads, then each A fragment's products and its next read
-        __builtin_amdgcn_sched_group_barrier(0x100, NF * (BX ? 2 : 1), 0);
+        if constexpr (F > 0) __builtin_amdgcn_sched_group_barrier(0x100, NF * (BX ? 2 : 1), 0);
 #pragma unroll
-        for (int i = 0; i < MF; ++i) {
+        for (int i = 0; i < F; ++i) {
           __builtin_amdgcn_sched_group_barrier(0x008, NF, 0);
           __builtin_amdgcn_sched_group_barrier(0x100, AX ? 2 : 1, 0);
         }
         __atomic_signal_fence(__ATOMIC_SEQ_CST);  // the reads stay in this slice
       });
     }
-  }
-  // each lane holds 4 consecutive columns (from 4 (lane / 16)) of row lane % 16 of a fragment
-  const int cols = P == kForward ? p.N : p.K;
-  const size_t row0 = P == kWgrad ? (size_t)t.e * p.N + t.m0 : (size_t)t.ra + t.m0;
+    // each lane holds 4 consecutive columns (from 4 (lane / 16)) of row lane % 16 of a fragment
 #pragma unroll
-  for (int i = 0; i < MF; ++i) {
-    const int r = wm + i * 16 + (lane & 15);
-    if (r >= t.mlim) continue;
+    for (int i = 0; i < F; ++i) {
+      const int r = wm + i * 16 + (lane & 15);
+      if (r >= t.mlim) continue;
 #pragma unroll
-    for (int j = 0; j < NF; ++j) {
-      const int c = wn + j * 16 + (lane >> 4) * 4;
-      if (c < t.clim) store4(p, (row0 + r) * cols + t.c0 + c, acc[i][j]);
+      for (int j = 0; j < NF; ++j) {
+        const int c = wn + j * 16 + (lane >> 4) * 4;
+        if (c < t.clim) store4(p, (row0 + r) * cols + t.c0 + c, acc[i][j]);
+      }
     }
+  };
+  if constexpr (DEAL) {
+    const int mine = __builtin_amdgcn_readfirstlane(min(MF, max(0, (t.mlim - wm + 15) / 16)));
+    static_for<MF + 1>([&](auto c) __attribute__((always_inline)) {
+      if (mine == decltype(c)::value) run(c);
+    });
+  } else {
+    run(std::integral_constant<int, MF>{});
   }
 }
 
@@ -462,10 +485,10 @@ long long tile_items(GroupedProduct kind, const GroupedGemmArgs& a, int TM, int 
   return (a.rows / TM + (a.E < a.rows ? a.E : a.rows)) * cols;
 }
 
-template <GroupedProduct P, int WM, int WN, int WGM, int WGN, int DK, int RING, bool ONCE>
+template <GroupedProduct P, int WM, int WN, int WGM, int WGN, int DK, int RING, bool ONCE, bool DEAL>
 hipError_t launch_tiles(const GroupedGemmArgs& a, const ProductArgs& p, hipStream_t stream) {
   const long long grid = xcd_grid(tile_items(P, a, WM * WGM, WN * WGN));
-  tile_kernel<P, WM, WN, WGM, WGN, DK, RING, ONCE><<<(unsigned)grid, 64 * WGM * WGN, 0, stream>>>(p);
+  tile_kernel<P, WM, WN, WGM, WGN, DK, RING, ONCE, DEAL><<<(unsigned)grid, 64 * WGM * WGN, 0, stream>>>(p);
   return hipGetLastError();
 }
 
@@ -480,13 +503,13 @@ hipError_t launch_product(const GroupedGemmArgs& a, hipStream_t stream) {
   }
   const long long mean = a.rows / a.E;  // rows per expert
   if constexpr (P == kWgrad) {
-    if (mean >= 128 && a.N > 128 && a.K > 128) return launch_tiles<P, 128, 64, 2, 4, 64, 2, false>(a, p, stream);
-    return launch_tiles<P, 64, 64, 2, 2, 64, 2, false>(a, p, stream);
+    if (mean >= 128 && a.N > 128 && a.K > 128) return launch_tiles<P, 128, 64, 2, 4, 64, 2, false, true>(a, p, stream);
+    return launch_tiles<P, 64, 64, 2, 2, 64, 2, false, false>(a, p, stream);
   } else {
-    if (mean >= 128) return launch_tiles<P, 128, 64, 2, 4, 64, 2, false>(a, p, stream);
-    if (mean >= 32) return launch_tiles<P, 64, 64, 2, 2, 64, 2, false>(a, p, stream);
-    if constexpr (P == kForward) return launch_tiles<P, 32, 16, 1, 4, 128, 4, true>(a, p, stream);
-    return launch_tiles<P, 32, 32, 1, 4, 64, 4, true>(a, p, stream);
+    if (mean >= 128) return launch_tiles<P, 128, 64, 2, 4, 64, 2, false, true>(a, p, stream);
+    if (mean >= 32) return launch_tiles<P, 64, 64, 2, 2, 64, 2, false, false>(a, p, stream);
+    if constexpr (P == kForward) return launch_tiles<P, 32, 16, 1, 4, 128, 4, true, false>(a, p, stream);
+    return launch_tiles<P, 32, 32, 1, 4, 64, 4, true, false>(a, p, stream);
   }
 }
 
