@@ -123,7 +123,7 @@ def _stream(stream):
 def _need(t, dtype, shape, name):
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != tuple(shape):
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
@@ -357,21 +357,33 @@ def moe_layer(logits, x, w_gate, w_up, w_down, k: int, out: dict, workspace: Wor
 # ----------------------------------------------------------------------------------------
 # training: the pieces of the layer's gradient (same names as the C ABI)
 # ----------------------------------------------------------------------------------------
-def _call(name: str, stream, tensors, args):
-    """Enqueue lib.<name>(*args, stream) on the device that every tensor is on, whichever is
-    current: on `stream`, or on that device's current stream."""
-    ptrs = {id(t): _ptr(t) for t in tensors if t is not None}
-    devices = {t.device for t in tensors if t is not None}
-    if len(devices) != 1:
-        raise ValueError("expected every tensor on one device")
-    device = devices.pop()
-    if stream is not None and stream.device != device:
+def _call(name: str, stream, *args):
+    """Enqueue lib.<name>(*args, stream), tensors among args as their addresses, on the device that
+    every tensor is on, whichever is current: on `stream`, or on that device's current stream."""
+    device = -1
+    raw = []
+    for a in args:
+        if isinstance(a, torch.Tensor):
+            if not a.is_cuda:
+                raise ValueError("expected a device tensor")
+            if not a.is_contiguous():
+                raise ValueError("expected a contiguous tensor")
+            d = a.get_device()
+            if d != device and device >= 0:
+                raise ValueError("expected every tensor on one device")
+            device = d
+            a = a.data_ptr()
+        raw.append(a)
+    if stream is not None and stream.device.index != device:
         raise ValueError("expected a stream of the tensors' device")
-    with torch.cuda.device(device):
-        if stream is None:
-            stream = torch.cuda.current_stream()
-        _check(getattr(load_library(), name)(*[ptrs[id(a)] if isinstance(a, torch.Tensor) else a for a in args],
-                                             _stream(stream)))
+    fn = getattr(_lib if _lib is not None else load_library(), name)
+    if device == torch.cuda.current_device():
+        status = fn(*raw, (stream or torch.cuda.current_stream()).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*raw, (stream or torch.cuda.current_stream()).cuda_stream)
+    if status != MOE_OK:
+        _check(status)
 
 
 def _float_dt(t, name):
@@ -402,8 +414,7 @@ def moe_grouped_gemm(x, offsets, w, y, stream=None):
     _need(w, x.dtype, (E, N, K), "w")
     _need(offsets, torch.int32, (E + 1,), "offsets")
     _need(y, y.dtype, (rows, N), "y")
-    _call("moe_grouped_gemm", stream, (x, offsets, w, y),
-          (x, _float_dt(x, "x"), offsets, rows, E, N, K, w, _float_dt(w, "w"), y, _float_dt(y, "y")))
+    _call("moe_grouped_gemm", stream, x, _float_dt(x, "x"), offsets, rows, E, N, K, w, _float_dt(w, "w"), y, _float_dt(y, "y"))
 
 
 def moe_grouped_gemm_dgrad(dy, offsets, w, dx, dy2=None, w2=None, stream=None):
@@ -419,9 +430,8 @@ def moe_grouped_gemm_dgrad(dy, offsets, w, dx, dy2=None, w2=None, stream=None):
     if dy2 is not None:
         _need(dy2, dy.dtype, (rows, N), "dy2")
         _need(w2, dy.dtype, (E, N, K), "w2")
-    _call("moe_grouped_gemm_dgrad", stream, (dy, dy2, offsets, w, w2, dx),
-          (dy, dy2, _float_dt(dy, "dy"), offsets, rows, E, N, K, w, w2, _float_dt(w, "w"), dx,
-           _float_dt(dx, "dx")))
+    _call("moe_grouped_gemm_dgrad", stream, dy, dy2, _float_dt(dy, "dy"), offsets, rows, E, N, K, w, w2, _float_dt(w, "w"), dx,
+          _float_dt(dx, "dx"))
 
 
 def moe_grouped_gemm_wgrad(dy, x, offsets, dw, accumulate: bool = False, stream=None):
@@ -433,8 +443,7 @@ def moe_grouped_gemm_wgrad(dy, x, offsets, dw, accumulate: bool = False, stream=
     _need(x, dy.dtype, (rows, K), "x")
     _need(offsets, torch.int32, (E + 1,), "offsets")
     _need(dw, dw.dtype, (E, N, K), "dw")
-    _call("moe_grouped_gemm_wgrad", stream, (dy, x, offsets, dw),
-          (dy, x, _float_dt(dy, "dy"), offsets, rows, E, N, K, dw, _float_dt(dw, "dw"), int(bool(accumulate))))
+    _call("moe_grouped_gemm_wgrad", stream, dy, x, _float_dt(dy, "dy"), offsets, rows, E, N, K, dw, _float_dt(dw, "dw"), int(bool(accumulate)))
 
 
 def moe_checkpoint_pack(x, codes, scales, stream=None):
@@ -442,7 +451,7 @@ def moe_checkpoint_pack(x, codes, scales, stream=None):
     scales [rows, ceil(d/128)] float32."""
     rows, d = _dims(x, 2, "x")
     _held(codes, scales, (rows, d), "x")
-    _call("moe_checkpoint_pack", stream, (x, codes, scales), (x, _float_dt(x, "x"), rows, d, codes, scales))
+    _call("moe_checkpoint_pack", stream, x, _float_dt(x, "x"), rows, d, codes, scales)
 
 
 def moe_checkpoint_unpack(codes, scales, out, flat_to_sorted=None, stream=None):
@@ -456,8 +465,7 @@ def moe_checkpoint_unpack(codes, scales, out, flat_to_sorted=None, stream=None):
     if T and rows % T:
         raise ValueError("flat_to_sorted must have k entries for every row")
     _need(out, out.dtype, (rows, d), "out")
-    _call("moe_checkpoint_unpack", stream, (codes, scales, flat_to_sorted, out),
-          (codes, scales, T, rows // T if T else 1, d, flat_to_sorted, out, _float_dt(out, "out")))
+    _call("moe_checkpoint_unpack", stream, codes, scales, T, rows // T if T else 1, d, flat_to_sorted, out, _float_dt(out, "out"))
 
 
 def moe_swiglu(g, u, h, g_codes=None, g_scales=None, u_codes=None, u_scales=None, offsets=None, stream=None):
@@ -473,8 +481,7 @@ def moe_swiglu(g, u, h, g_codes=None, g_scales=None, u_codes=None, u_scales=None
         _held(g_codes, g_scales, (rows, f), "g")
         _held(u_codes, u_scales, (rows, f), "u")
     E = _row_offsets(offsets)
-    _call("moe_swiglu", stream, (g, u, offsets, h, *held),
-          (g, u, _float_dt(g, "g"), offsets, E, rows, f, h, *held))
+    _call("moe_swiglu", stream, g, u, _float_dt(g, "g"), offsets, E, rows, f, h, *held)
 
 
 def _row_offsets(offsets) -> int:
@@ -503,8 +510,7 @@ def moe_swiglu_backward(dh, g, u, dg, du, h=None, g_scales=None, u_scales=None, 
         _held(u, u_scales, (rows, f), "u")
         gu = MOE_FP8_E4M3FN
     E = _row_offsets(offsets)
-    _call("moe_swiglu_backward", stream, (dh, g, u, g_scales, u_scales, offsets, dg, du, h),
-          (dh, _float_dt(dh, "dh"), g, u, gu, g_scales, u_scales, offsets, E, rows, f, dg, du, h))
+    _call("moe_swiglu_backward", stream, dh, _float_dt(dh, "dh"), g, u, gu, g_scales, u_scales, offsets, E, rows, f, dg, du, h)
 
 
 def moe_combine_backward(dy, y_sorted, flat_to_sorted, topk_gates, dy_sorted, dgates, stream=None):
@@ -520,9 +526,8 @@ def moe_combine_backward(dy, y_sorted, flat_to_sorted, topk_gates, dy_sorted, dg
     if dgates is not None:
         _need(y_sorted, torch.float32, (T * k, d), "y_sorted")
         _need(dgates, torch.float32, (T, k), "dgates")
-    _call("moe_combine_backward", stream, (dy, y_sorted, flat_to_sorted, topk_gates, dy_sorted, dgates),
-          (dy, _float_dt(dy, "dy"), y_sorted, flat_to_sorted, topk_gates, T, k, d, dy_sorted,
-           _float_dt(dy_sorted, "dy_sorted"), dgates))
+    _call("moe_combine_backward", stream, dy, _float_dt(dy, "dy"), y_sorted, flat_to_sorted, topk_gates, T, k, d, dy_sorted,
+          _float_dt(dy_sorted, "dy_sorted"), dgates)
 
 
 def moe_permute_backward(dx_sorted, flat_to_sorted, k: int, dx, stream=None):
@@ -530,8 +535,7 @@ def moe_permute_backward(dx_sorted, flat_to_sorted, k: int, dx, stream=None):
     T, d = _dims(dx, 2, "dx")
     _need(dx_sorted, dx_sorted.dtype, (T * k, d), "dx_sorted")
     _need(flat_to_sorted, torch.int32, (T * k,), "flat_to_sorted")
-    _call("moe_permute_backward", stream, (dx_sorted, flat_to_sorted, dx),
-          (dx_sorted, _float_dt(dx_sorted, "dx_sorted"), flat_to_sorted, T, k, d, dx, _float_dt(dx, "dx")))
+    _call("moe_permute_backward", stream, dx_sorted, _float_dt(dx_sorted, "dx_sorted"), flat_to_sorted, T, k, d, dx, _float_dt(dx, "dx"))
 
 
 def moe_route_backward(dgates, topk_ids, topk_gates, dlogits, stream=None):
@@ -542,8 +546,7 @@ def moe_route_backward(dgates, topk_ids, topk_gates, dlogits, stream=None):
     _need(topk_ids, torch.int32, (T, k), "topk_ids")
     _need(topk_gates, torch.float32, (T, k), "topk_gates")
     _need(dlogits, torch.float32, (T, E), "dlogits")
-    _call("moe_route_backward", stream, (dgates, topk_ids, topk_gates, dlogits),
-          (dgates, topk_ids, topk_gates, T, E, k, dlogits))
+    _call("moe_route_backward", stream, dgates, topk_ids, topk_gates, T, E, k, dlogits)
 
 
 def layer_buffers(T: int, E: int, k: int, d: int, act_dtype, device="cuda",
