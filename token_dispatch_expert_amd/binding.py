@@ -377,11 +377,13 @@ def _call(name: str, stream, *args):
     if stream is not None and stream.device.index != device:
         raise ValueError("expected a stream of the tensors' device")
     fn = getattr(_lib if _lib is not None else load_library(), name)
+    # (the raw handle of the current stream: 0.2 us, against 2.7 for torch.cuda.current_stream())
+    handle = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
     if device == torch.cuda.current_device():
-        status = fn(*raw, (stream or torch.cuda.current_stream()).cuda_stream)
+        status = fn(*raw, handle)
     else:
         with torch.cuda.device(device):
-            status = fn(*raw, (stream or torch.cuda.current_stream()).cuda_stream)
+            status = fn(*raw, handle)
     if status != MOE_OK:
         _check(status)
 

@@ -38,7 +38,7 @@ __global__ __launch_bounds__(kRowThreads) void pack_kernel(RowMap m, const T* __
 
 // Row t of the codes to each of its k rows of the output (flat_to_sorted; entries that name no
 // row are skipped), or to row t itself without a map. The codes are read once, for all k.
-template <typename T>
+template <typename T, bool WIDE>
 __global__ __launch_bounds__(kRowThreads) void unpack_kernel(RowMap m, const uint8_t* __restrict__ codes,
                                                             const float* __restrict__ scales, int T_,
                                                             int k, int d,
@@ -46,19 +46,19 @@ __global__ __launch_bounds__(kRowThreads) void unpack_kernel(RowMap m, const uin
                                                             T* __restrict__ out) {
   unsigned t;
   int unit;
-  row_unit(m, t, unit);
+  row_unit<WIDE>(m, t, unit);
   if (t >= (unsigned)T_ || unit * 8 >= d) return;
   const uint2 c = *reinterpret_cast<const uint2*>(codes + (size_t)t * d + unit * 8);
   const float scale = scales[(size_t)t * ((d + kHeldGroup - 1) / kHeldGroup) + unit / 16];
   const F8 v = held8(c, scale);
   if (!f2s) {
-    store8(out + (size_t)t * d + unit * 8, v);
+    store8_once(out + (size_t)t * d + unit * 8, v);
     return;
   }
   const int R = T_ * k;
   for (int j = 0; j < k; ++j) {
     const int p = f2s[(size_t)t * k + j];
-    if ((unsigned)p < (unsigned)R) store8(out + (size_t)p * d + unit * 8, v);
+    if ((unsigned)p < (unsigned)R) store8_once(out + (size_t)p * d + unit * 8, v);
   }
 }
 
@@ -72,6 +72,15 @@ struct SwigluArgs {
   int E, rows, f;
 };
 
+// 1 / (1 + e^-g). For bf16 results the hardware's exp2 and reciprocal (each within one unit of
+// fp32, and the product with log2 e within |g| 2^-24) are far inside the result's rounding;
+// e^-g past the range gives 0, the limit.
+template <typename T>
+__device__ __forceinline__ float sigmoid(float g) {
+  if constexpr (sizeof(T) == 2) return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504088896f));
+  else return 1.0f / (1.0f + expf(-g));
+}
+
 template <typename T>
 __global__ __launch_bounds__(kRowThreads) void swiglu_kernel(RowMap m, SwigluArgs p) {
   unsigned row;
@@ -80,8 +89,8 @@ __global__ __launch_bounds__(kRowThreads) void swiglu_kernel(RowMap m, SwigluArg
   if (row >= (unsigned)rows_in_use(p.offsets, p.E, p.rows)) return;
   const bool in = unit * 8 < p.f;
   const size_t at = (size_t)row * p.f + unit * 8;
-  const F8 g = in ? load8(static_cast<const T*>(p.g) + at) : F8{};
-  const F8 u = in ? load8(static_cast<const T*>(p.u) + at) : F8{};
+  const F8 g = in ? load8_once(static_cast<const T*>(p.g) + at) : F8{};
+  const F8 u = in ? load8_once(static_cast<const T*>(p.u) + at) : F8{};
   if (p.gc) {
     float gs, us;
     const uint2 cg = hold8(g, gs), cu = hold8(u, us);
@@ -98,8 +107,8 @@ __global__ __launch_bounds__(kRowThreads) void swiglu_kernel(RowMap m, SwigluArg
   if (!in) return;
   F8 h;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) h.v[i] = g.v[i] / (1.0f + expf(-g.v[i])) * u.v[i];
-  store8(static_cast<T*>(p.h) + at, h);
+  for (int i = 0; i < 8; ++i) h.v[i] = g.v[i] * sigmoid<T>(g.v[i]) * u.v[i];
+  store8_once(static_cast<T*>(p.h) + at, h);
 }
 
 template <typename T, bool HELD>
@@ -115,22 +124,22 @@ __global__ __launch_bounds__(kRowThreads) void swiglu_backward_kernel(RowMap m, 
     g = held8(*reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.g) + at), p.gs[s]);
     u = held8(*reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.u) + at), p.us[s]);
   } else {
-    g = load8(static_cast<const T*>(p.g) + at);
-    u = load8(static_cast<const T*>(p.u) + at);
+    g = load8_once(static_cast<const T*>(p.g) + at);
+    u = load8_once(static_cast<const T*>(p.u) + at);
   }
-  const F8 dh = load8(static_cast<const T*>(p.dh) + at);
+  const F8 dh = load8_once(static_cast<const T*>(p.dh) + at);
   F8 dg, du, h;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float s = 1.0f / (1.0f + expf(-g.v[i]));
+    const float s = sigmoid<T>(g.v[i]);
     const float silu = g.v[i] * s;
     h.v[i] = silu * u.v[i];
     du.v[i] = dh.v[i] * silu;
     dg.v[i] = dh.v[i] * u.v[i] * s * (1.0f + g.v[i] * (1.0f - s));
   }
-  store8(static_cast<T*>(p.dg) + at, dg);
-  store8(static_cast<T*>(p.du) + at, du);
-  if (p.h) store8(static_cast<T*>(p.h) + at, h);
+  store8_once(static_cast<T*>(p.dg) + at, dg);
+  store8_once(static_cast<T*>(p.du) + at, du);
+  if (p.h) store8_once(static_cast<T*>(p.h) + at, h);
 }
 
 }  // namespace
@@ -143,23 +152,26 @@ hipError_t launch_pack(const void* x, bool bf16, int rows, int d, void* codes, f
   const unsigned grid = (unsigned)row_grid(m, rows);
   uint8_t* c = static_cast<uint8_t*>(codes);
   if (bf16)
-    pack_kernel<<<grid, kRowThreads, 0, stream>>>(m, static_cast<const __bf16*>(x), rows, d, c, scales);
+    pack_kernel<<<grid, m.threads(), 0, stream>>>(m, static_cast<const __bf16*>(x), rows, d, c, scales);
   else
-    pack_kernel<<<grid, kRowThreads, 0, stream>>>(m, static_cast<const float*>(x), rows, d, c, scales);
+    pack_kernel<<<grid, m.threads(), 0, stream>>>(m, static_cast<const float*>(x), rows, d, c, scales);
+  return hipGetLastError();
+}
+
+template <typename T>
+static hipError_t launch_unpack_t(const void* codes, const float* scales, int T_, int k, int d, const int32_t* f2s,
+                                  void* out, hipStream_t stream) {
+  const RowMap m = row_map(d / 8);
+  auto kern = m.shift >= 6 ? &unpack_kernel<T, true> : &unpack_kernel<T, false>;
+  kern<<<(unsigned)row_grid(m, T_), m.threads(), 0, stream>>>(m, static_cast<const uint8_t*>(codes), scales, T_, k, d,
+                                                              f2s, static_cast<T*>(out));
   return hipGetLastError();
 }
 
 hipError_t launch_unpack(const void* codes, const float* scales, int T, int k, int d, const int32_t* f2s,
                          void* out, bool bf16, hipStream_t stream) {
   if (T == 0) return hipSuccess;
-  const RowMap m = row_map(d / 8);
-  const unsigned grid = (unsigned)row_grid(m, T);
-  const uint8_t* c = static_cast<const uint8_t*>(codes);
-  if (bf16)
-    unpack_kernel<<<grid, kRowThreads, 0, stream>>>(m, c, scales, T, k, d, f2s, static_cast<__bf16*>(out));
-  else
-    unpack_kernel<<<grid, kRowThreads, 0, stream>>>(m, c, scales, T, k, d, f2s, static_cast<float*>(out));
-  return hipGetLastError();
+  return (bf16 ? &launch_unpack_t<__bf16> : &launch_unpack_t<float>)(codes, scales, T, k, d, f2s, out, stream);
 }
 
 hipError_t launch_swiglu(const void* g, const void* u, bool bf16, const int32_t* offsets, int E, int rows,
@@ -174,9 +186,9 @@ hipError_t launch_swiglu(const void* g, const void* u, bool bf16, const int32_t*
   const RowMap m = row_map((f + 127) / 128 * 16);
   const unsigned grid = (unsigned)row_grid(m, rows);
   if (bf16)
-    swiglu_kernel<__bf16><<<grid, kRowThreads, 0, stream>>>(m, p);
+    swiglu_kernel<__bf16><<<grid, m.threads(), 0, stream>>>(m, p);
   else
-    swiglu_kernel<float><<<grid, kRowThreads, 0, stream>>>(m, p);
+    swiglu_kernel<float><<<grid, m.threads(), 0, stream>>>(m, p);
   return hipGetLastError();
 }
 
@@ -192,7 +204,7 @@ hipError_t launch_swiglu_backward(const void* dh, bool bf16, const void* g, cons
   const unsigned grid = (unsigned)row_grid(m, rows);
   auto kern = bf16 ? (held ? &swiglu_backward_kernel<__bf16, true> : &swiglu_backward_kernel<__bf16, false>)
                    : (held ? &swiglu_backward_kernel<float, true> : &swiglu_backward_kernel<float, false>);
-  kern<<<grid, kRowThreads, 0, stream>>>(m, p);
+  kern<<<grid, m.threads(), 0, stream>>>(m, p);
   return hipGetLastError();
 }
 
