@@ -21,29 +21,22 @@ namespace moe {
 namespace {
 
 // ---------------------------------------------------------------------------------------
-// Tiles staged through registers, fp32 matrix instructions
+// fp32: tiles staged through registers
 // ---------------------------------------------------------------------------------------
 // A workgroup of 4 waves (2 x 2) computes a TM x TM tile of C; the contraction goes in steps of
-// 32. Both operands lie in LDS as fp32 in their memory order: along operands [m][32 + 4],
+// 32. Both operands lie in LDS in their memory order: along operands [m][32 + 4],
 // across operands [32][m + 4]; the padding of 4 floats puts the 16 rows (or 4 row groups) of a
 // fragment read on distinct banks. v_mfma_f32_16x16x4_f32 takes one contraction element per
 // lane (row or column lane % 16, element lane / 16); lane group g takes elements 4g .. 4g + 3
 // of a 16-long slice in turn, the same for both operands, so an along fragment is one 16-byte
 // read. The operands go in as (B, A), which gives each lane 4 consecutive columns of one row of
 // C: one 16-byte (fp32) or 8-byte (bf16) store.
+// Bound by the matrix instructions: 16,384 rows over 8 experts of 1024 x 2048 take 634 us forward
+// (108 TFLOP/s; a large fp32 library product reaches 132), 1.21 ms for two input gradients, 617 us
+// for the weight gradient. Tiles of 128 measured slower at every size (693, 1380 and 736 us).
 constexpr int kStep = 32;
 constexpr int kPad = 4;
 constexpr int kF32Tile = 64;
-
-template <typename T> struct Chunk;  // 4 elements as stored
-template <> struct Chunk<float> { float4 v; };
-template <> struct Chunk<__bf16> { uint2 v; };
-
-__device__ __forceinline__ float4 widen(const Chunk<float>& c) { return c.v; }
-__device__ __forceinline__ float4 widen(const Chunk<__bf16>& c) {
-  return make_float4(__uint_as_float(c.v.x << 16), __uint_as_float(c.v.x & 0xffff0000u),
-                     __uint_as_float(c.v.y << 16), __uint_as_float(c.v.y & 0xffff0000u));
-}
 
 struct ProductArgs {
   const void *a, *b, *a2, *b2;  // a2, b2: second pair of operands (dgrad), or null
@@ -116,24 +109,24 @@ __device__ __forceinline__ bool tile_at(const ProductArgs& p, int TM, int TN, Ti
 // contraction. base: the operand's first element of the tile; lim: rows or columns of the tile
 // that exist; ld: its row stride; k0, kdim: the step's first contraction element and their
 // number. What lies outside reads as zero.
-template <typename T, bool ACROSS, int TM>
+template <bool ACROSS, int TM>
 struct Stage {
-  static constexpr int NCH = TM * kStep / 4 / 256;  // chunks per thread
-  Chunk<T> c[NCH];
+  static constexpr int NCH = TM * kStep / 4 / 256;  // 4-element chunks per thread
+  float4 c[NCH];
   __device__ __forceinline__ static void at(int i, int& outer, int& inner) {
     const int q = threadIdx.x + i * 256;
     constexpr int per = (ACROSS ? TM : kStep) / 4;  // chunks per LDS row
     outer = q / per;
     inner = q % per * 4;
   }
-  __device__ __forceinline__ void load(const T* base, int lim, int ld, int k0, int kdim) {
+  __device__ __forceinline__ void load(const float* base, int lim, int ld, int k0, int kdim) {
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
       int o, n;
       at(i, o, n);
       const bool ok = ACROSS ? (k0 + o < kdim && n < lim) : (o < lim && k0 + n < kdim);
       const size_t e = ACROSS ? (size_t)(k0 + o) * ld + n : (size_t)o * ld + k0 + n;
-      c[i] = ok ? *reinterpret_cast<const Chunk<T>*>(base + e) : Chunk<T>{};
+      c[i] = ok ? *reinterpret_cast<const float4*>(base + e) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
   }
   __device__ __forceinline__ void put(float* lds) const {
@@ -142,7 +135,7 @@ struct Stage {
     for (int i = 0; i < NCH; ++i) {
       int o, n;
       at(i, o, n);
-      *reinterpret_cast<float4*>(lds + o * row + n) = widen(c[i]);
+      *reinterpret_cast<float4*>(lds + o * row + n) = c[i];
     }
   }
 };
@@ -161,8 +154,8 @@ __device__ __forceinline__ f32x4 fragment(const float* lds, int m, int k) {
 template <bool ACROSS, int TM>
 constexpr int stage_floats() { return ACROSS ? kStep * (TM + kPad) : TM * (kStep + kPad); }
 
-template <typename T, GroupedProduct P, int TM>
-__global__ __launch_bounds__(256) void product_kernel(ProductArgs p) {
+template <GroupedProduct P, int TM>
+__global__ __launch_bounds__(256) void f32_kernel(ProductArgs p) {
   constexpr bool AX = P == kWgrad, BX = P != kForward;
   constexpr int FR = TM / 32;  // 16-wide fragments per wave and side
   __shared__ __align__(16) float la[stage_floats<AX, TM>()];
@@ -180,21 +173,24 @@ __global__ __launch_bounds__(256) void product_kernel(ProductArgs p) {
   const size_t b_at = P == kForward ? wbase + (size_t)c0 * p.K
                       : P == kDgrad ? wbase + c0 : (size_t)ra * p.K + c0;
 
-  f32x4 acc[FR][FR];
+  // Sums in two levels: `acc` over kRun steps, `sum` over those. One chain of K / 4 additions was
+  // twice as far from the 64-bit result at K = 4096.
+  constexpr int kRun = 8;
+  f32x4 acc[FR][FR], sum[FR][FR];
 #pragma unroll
   for (int i = 0; i < FR; ++i)
 #pragma unroll
-    for (int j = 0; j < FR; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < FR; ++j) acc[i][j] = sum[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   const int steps1 = (kdim + kStep - 1) / kStep;
   const int steps = (P == kDgrad && p.a2) ? 2 * steps1 : steps1;
-  Stage<T, AX, TM> sa;
-  Stage<T, BX, TM> sb;
+  Stage<AX, TM> sa;
+  Stage<BX, TM> sb;
   auto load = [&](int st) __attribute__((always_inline)) {
     const bool second = st >= steps1;
     const int k0 = (second ? st - steps1 : st) * kStep;
-    sa.load(static_cast<const T*>(second ? p.a2 : p.a) + a_at, mlim, lda, k0, kdim);
-    sb.load(static_cast<const T*>(second ? p.b2 : p.b) + b_at, clim, p.K, k0, kdim);
+    sa.load(static_cast<const float*>(second ? p.a2 : p.a) + a_at, mlim, lda, k0, kdim);
+    sb.load(static_cast<const float*>(second ? p.b2 : p.b) + b_at, clim, p.K, k0, kdim);
   };
   if (steps > 0) load(0);
   for (int st = 0; st < steps; ++st) {
@@ -219,6 +215,15 @@ __global__ __launch_bounds__(256) void product_kernel(ProductArgs p) {
           for (int j = 0; j < FR; ++j)
             acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(fb[j][q], fa[i][q], acc[i][j], 0, 0, 0);
     }
+    if (st % kRun == kRun - 1 || st == steps - 1) {
+#pragma unroll
+      for (int i = 0; i < FR; ++i)
+#pragma unroll
+        for (int j = 0; j < FR; ++j) {
+          sum[i][j] += acc[i][j];
+          acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+    }
   }
   const size_t crow0 = P == kWgrad ? (size_t)e * p.N + m0 : (size_t)ra + m0;
 #pragma unroll
@@ -228,7 +233,7 @@ __global__ __launch_bounds__(256) void product_kernel(ProductArgs p) {
 #pragma unroll
     for (int j = 0; j < FR; ++j) {
       const int c = (wn * FR + j) * 16 + (lane >> 4) * 4;
-      if (c < clim) store4(p, (crow0 + r) * cols + c0 + c, acc[i][j]);
+      if (c < clim) store4(p, (crow0 + r) * cols + c0 + c, sum[i][j]);
     }
   }
 }
@@ -342,18 +347,15 @@ __device__ __forceinline__ void bare_barrier() {
   __atomic_signal_fence(__ATOMIC_SEQ_CST);
 }
 
-// 16 consecutive bytes of a row of C per lane and store. `v` holds a wave's 16 rows of WN columns
-// as the products leave them: 4 consecutive columns (from 4 (lane / 16)) of row lane % 16 in each
-// 16-column fragment. Stored like that, an instruction writes 64 bytes (fp32) or 32 (bf16) of
-// each of 16 rows; here lanes first exchange parts so that it writes 128 bytes of each of 8 rows.
-__device__ __forceinline__ u32x4 rotate8(u32x4 v) {  // from the lane 8 further in the 16
+// The value of the lane 8 further within the 16.
+__device__ __forceinline__ u32x4 rotate8(u32x4 v) {
   u32x4 r;
 #pragma unroll
   for (int q = 0; q < 4; ++q) r[q] = (unsigned)__builtin_amdgcn_mov_dpp((int)v[q], 0x128, 0xf, 0xf, true);
   return r;
 }
-// a: this lane's part of the row's first 64 bytes, b: of the next 64. put(row, part, v): 16 bytes
-// of `row` of the 16, part 0 from the first 64 bytes or 1.
+// 16 rows of which a lane holds 16 bytes of row lane % 16 in each of two 64-byte parts, a and b, to
+// 8 whole 128-byte pieces twice: put(row, part, v) gets 16 bytes of that row's part 0 or 1.
 template <typename F>
 __device__ __forceinline__ void store_row_halves(u32x4 a, u32x4 b, int lane, F&& put) {
   const bool low = (lane & 8) == 0;
@@ -385,7 +387,10 @@ struct OutTile {
   __device__ __forceinline__ int at(int r, int c, int size) const { return c < clim ? r * ld + c * size : kOutside; }
 };
 
-// One 16-row fragment row of C, rows from r0 and NF * 16 columns from c0 of the tile.
+// 16 rows of C from r0 and NF * 16 columns from c0 of the tile. `v` is as the products leave it: 4
+// consecutive columns (from 4 (lane / 16)) of row lane % 16 in each 16-column fragment. Stored
+// like that, an instruction would write 64 bytes (fp32) or 32 (bf16) of each of 16 rows; lanes
+// first exchange parts so that it writes 128 bytes of each of 8 (2% of the large products' time).
 template <int NF>
 __device__ __forceinline__ void store_fragments(const OutTile& o, const ProductArgs& p, const f32x4 (&v)[NF], int r0,
                                                 int c0, int lane) {
@@ -594,7 +599,7 @@ hipError_t launch_product(const GroupedGemmArgs& a, hipStream_t stream) {
                       a.out_bf16 ? 1 : 0, a.accumulate ? 1 : 0};
   if (!a.bf16) {
     const long long grid = xcd_grid(tile_items(P, a, kF32Tile, kF32Tile));
-    product_kernel<float, P, kF32Tile><<<(unsigned)grid, 256, 0, stream>>>(p);
+    f32_kernel<P, kF32Tile><<<(unsigned)grid, 256, 0, stream>>>(p);
     return hipGetLastError();
   }
   // Which tiles, from the sizes alone (the host does not know the offsets). Measured at 64 experts of
