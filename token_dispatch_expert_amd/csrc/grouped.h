@@ -97,37 +97,4 @@ __device__ __forceinline__ bool find_row_tile(const int32_t* offsets, int E, int
   return true;
 }
 
-// The expert of rank r when experts are ordered by their number of rows, the most first, to
-// within a factor of two (equal powers of two keep the expert order). Work whose cost goes
-// with an expert's rows then starts with the longest.
-__device__ __forceinline__ int expert_of_rank(const int32_t* offsets, int E, int rows, int r) {
-  const int lane = threadIdx.x & 63;
-  int key[16];  // E <= MOE_MAX_EXPERTS = 1024
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    key[i] = -1;
-    const int x = lane + 64 * i;
-    if (64 * i < E && x < E) {
-      int a, b;
-      group_rows(offsets, x, rows, a, b);
-      key[i] = 32 - __clz(b - a);
-    }
-  }
-  int before = 0;
-  for (int k = 31; k >= 0; --k) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      if (64 * i >= E) break;
-      unsigned long long m = __ballot(key[i] == k);
-      const int n = __popcll(m);
-      if (r < before + n) {
-        for (int s = r - before; s > 0; --s) m &= m - 1;
-        return __builtin_amdgcn_readfirstlane(64 * i + __ffsll(m) - 1);
-      }
-      before += n;
-    }
-  }
-  return 0;  // not reached for r < E
-}
-
 }  // namespace moe

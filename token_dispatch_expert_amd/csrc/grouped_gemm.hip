@@ -80,10 +80,12 @@ __device__ __forceinline__ bool tile_at(const ProductArgs& p, int TM, int TN, Ti
   if constexpr (P == kWgrad) {
     const long long per = (long long)((p.N + TM - 1) / TM) * CT;
     if (item >= p.E * per) return false;
-    const int local = (int)(item % per);
-    t.e = expert_of_rank(p.offsets, p.E, p.rows, (int)(item / per));
+    // Experts in their order: starting with those of the most rows cost 3 to 12%, whichever way the
+    // rows were dealt (64 experts, Zipf 1.2: 444 against 396 us). Side by side, tiles of different
+    // lengths do not all store at the same time.
+    t.e = (int)(item / per);
     group_rows(p.offsets, t.e, p.rows, t.ra, t.rb);
-    tile_pair(local, (p.N + TM - 1) / TM, CT, mt, nt);
+    tile_pair((int)(item % per), (p.N + TM - 1) / TM, CT, mt, nt);
     if (t.ra == t.rb && p.accumulate) return false;
   } else {
     if (!find_row_tile(p.offsets, p.E, p.rows, TM, CT, item, t.e, t.ra, t.rb, mt, nt)) return false;
