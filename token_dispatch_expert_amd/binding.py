@@ -360,18 +360,19 @@ def moe_layer(logits, x, w_gate, w_up, w_down, k: int, out: dict, workspace: Wor
 def _call(name: str, stream, *args):
     """Enqueue lib.<name>(*args, stream), tensors among args as their addresses, on the device that
     every tensor is on, whichever is current: on `stream`, or on that device's current stream."""
-    device = -1
+    device = None
     raw = []
     for a in args:
         if isinstance(a, torch.Tensor):
-            if not a.is_cuda:
-                raise ValueError("expected a device tensor")
+            d = a.get_device()
+            if d != device:
+                if d < 0:
+                    raise ValueError("expected a device tensor")
+                if device is not None:
+                    raise ValueError("expected every tensor on one device")
+                device = d
             if not a.is_contiguous():
                 raise ValueError("expected a contiguous tensor")
-            d = a.get_device()
-            if d != device and device >= 0:
-                raise ValueError("expected every tensor on one device")
-            device = d
             a = a.data_ptr()
         raw.append(a)
     if stream is not None and stream.device.index != device:

@@ -29,8 +29,7 @@ namespace {
 // fragment read on distinct banks. v_mfma_f32_16x16x4_f32 takes one contraction element per
 // lane (row or column lane % 16, element lane / 16); lane group g takes elements 4g .. 4g + 3
 // of a 16-long slice in turn, the same for both operands, so an along fragment is one 16-byte
-// read. The operands go in as (B, A), which gives each lane 4 consecutive columns of one row of
-// C: one 16-byte (fp32) or 8-byte (bf16) store.
+// read. The operands go in as (B, A), which gives each lane 4 consecutive columns of one row of C.
 // Bound by the matrix instructions: 16,384 rows over 8 experts of 1024 x 2048 take 634 us forward
 // (108 TFLOP/s; a large fp32 library product reaches 132), 1.21 ms for two input gradients, 617 us
 // for the weight gradient. Tiles of 128 measured slower at every size (693, 1380 and 736 us).
@@ -46,23 +45,111 @@ struct ProductArgs {
   int out_bf16, accumulate;
 };
 
-// One row's 4 consecutive columns of C.
-__device__ __forceinline__ void store4(const ProductArgs& p, size_t at, f32x4 v) {
-  if (p.out_bf16) {
-    bf16x4* o = reinterpret_cast<bf16x4*>(static_cast<__bf16*>(p.out) + at);
-    if (p.accumulate) {
-      const bf16x4 old = *o;
+// The value of the lane 8 further within the 16.
+__device__ __forceinline__ u32x4 rotate8(u32x4 v) {
+  u32x4 r;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] += (float)old[j];
-    }
-    *o = bf16x4{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
-  } else {
-    f32x4* o = reinterpret_cast<f32x4*>(static_cast<float*>(p.out) + at);
-    if (p.accumulate) v += *o;
-    *o = v;
-  }
+  for (int q = 0; q < 4; ++q) r[q] = (unsigned)__builtin_amdgcn_mov_dpp((int)v[q], 0x128, 0xf, 0xf, true);
+  return r;
+}
+// 16 rows of which a lane holds 16 bytes of row lane % 16 in each of two 64-byte parts, a and b, to
+// 8 whole 128-byte pieces twice: put(row, part, v) gets 16 bytes of that row's part 0 or 1.
+template <typename F>
+__device__ __forceinline__ void store_row_halves(u32x4 a, u32x4 b, int lane, F&& put) {
+  const bool low = (lane & 8) == 0;
+  const u32x4 moved = rotate8(low ? b : a);
+  put(lane & 7, low ? 0 : 1, low ? a : moved);
+  put((lane & 7) + 8, low ? 0 : 1, low ? moved : b);
+}
+__device__ __forceinline__ unsigned pack_bf16(float a, float b) {
+  const bf16x2 v{(__bf16)a, (__bf16)b};
+  return __builtin_bit_cast(unsigned, v);
 }
 
+// The part of a tile of C that a wave stores. Stores go through a buffer descriptor that ends
+// with the tile's last row, and lanes past the last column aim behind it, so what lies outside
+// is dropped without a branch.
+struct OutTile {
+  __amdgpu_buffer_rsrc_t to;
+  int ld, clim;  // bytes of a row of C; columns that exist
+  static constexpr int kOutside = (int)0x80000000u;
+
+  // rows from row0 (mlim of them exist) and columns from c0 of out [.., cols]
+  __device__ __forceinline__ void set(const ProductArgs& p, size_t row0, int mlim, int c0, int clim_, int cols) {
+    const int size = p.out_bf16 ? 2 : 4;
+    ld = cols * size;
+    clim = clim_;
+    to = __builtin_amdgcn_make_buffer_rsrc(static_cast<char*>(p.out) + (row0 * cols + c0) * size, (short)0,
+                                           mlim * ld - c0 * size, kBufferWord3);
+  }
+  __device__ __forceinline__ int at(int r, int c, int size) const { return c < clim ? r * ld + c * size : kOutside; }
+};
+
+// 16 rows of C from r0 and NF * 16 columns from c0 of the tile. `v` is as the products leave it: 4
+// consecutive columns (from 4 (lane / 16)) of row lane % 16 in each 16-column fragment. Stored
+// like that, an instruction would write 64 bytes (fp32) or 32 (bf16) of each of 16 rows; lanes
+// first exchange parts so that it writes 128 bytes of each of 8 (2% of the large products' time),
+// non-temporal, which leaves the L2 to the operands (weight gradients of 128 rows per expert: 526
+// against 424 us).
+template <int NF>
+__device__ __forceinline__ void store_fragments(const OutTile& o, const ProductArgs& p, const f32x4 (&v)[NF], int r0,
+                                                int c0, int lane) {
+  if constexpr (NF % 2 == 0) {
+    if (!p.accumulate && !p.out_bf16) {
+#pragma unroll
+      for (int j = 0; j < NF; j += 2)
+        store_row_halves(__builtin_bit_cast(u32x4, v[j]), __builtin_bit_cast(u32x4, v[j + 1]), lane,
+                         [&](int r, int part, u32x4 x) __attribute__((always_inline)) {
+                           const int c = c0 + (j + part) * 16 + (lane >> 4) * 4;
+                           __builtin_amdgcn_raw_buffer_store_b128(x, o.to, o.at(r0 + r, c, 4), 0, kNonTemporal);
+                         });
+      return;
+    }
+  }
+  if constexpr (NF % 4 == 0) {
+    if (!p.accumulate) {
+      u32x4 q[NF / 2];  // 8 columns of fragment j (even lane groups) or j + 1 (odd ones)
+#pragma unroll
+      for (int j = 0; j < NF; j += 2)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const auto s = __builtin_amdgcn_permlane16_swap(pack_bf16(v[j][2 * h], v[j][2 * h + 1]),
+                                                          pack_bf16(v[j + 1][2 * h], v[j + 1][2 * h + 1]), false, false);
+          q[j / 2][h] = s[0];
+          q[j / 2][2 + h] = s[1];
+        }
+#pragma unroll
+      for (int j = 0; j < NF / 2; j += 2)
+        store_row_halves(q[j], q[j + 1], lane, [&](int r, int part, u32x4 x) __attribute__((always_inline)) {
+          const int g = lane >> 4;
+          const int c = c0 + (j + part) * 32 + (g & 1) * 16 + (g >> 1) * 8;
+          __builtin_amdgcn_raw_buffer_store_b128(x, o.to, o.at(r0 + r, c, 2), 0, kNonTemporal);
+        });
+      return;
+    }
+  }
+  const int r = r0 + (lane & 15);
+#pragma unroll
+  for (int j = 0; j < NF; ++j) {
+    const int c = c0 + j * 16 + (lane >> 4) * 4;
+    f32x4 x = v[j];
+    if (p.out_bf16) {
+      const int at = o.at(r, c, 2);
+      if (p.accumulate) {
+        const u32x2 old = __builtin_amdgcn_raw_buffer_load_b64(o.to, at, 0, 0);
+        x[0] += __uint_as_float(old[0] << 16);
+        x[1] += __uint_as_float(old[0] & 0xffff0000u);
+        x[2] += __uint_as_float(old[1] << 16);
+        x[3] += __uint_as_float(old[1] & 0xffff0000u);
+      }
+      __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])}, o.to, at, 0, 0);
+    } else {
+      const int at = o.at(r, c, 4);
+      if (p.accumulate) x += __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(o.to, at, 0, 0));
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), o.to, at, 0, 0);
+    }
+  }
+}
 // Where a tile lies: expert, its rows [ra, rb), C's rows from m0 (of mlim in the tile) and
 // columns from c0 (of clim), and the contraction's length.
 struct TileAt {
@@ -227,17 +314,10 @@ __global__ __launch_bounds__(256) void f32_kernel(ProductArgs p) {
         }
     }
   }
-  const size_t crow0 = P == kWgrad ? (size_t)e * p.N + m0 : (size_t)ra + m0;
+  OutTile o;
+  o.set(p, P == kWgrad ? (size_t)e * p.N + m0 : (size_t)ra + m0, mlim, c0, clim, cols);
 #pragma unroll
-  for (int i = 0; i < FR; ++i) {
-    const int r = (wm * FR + i) * 16 + (lane & 15);
-    if (r >= mlim) continue;
-#pragma unroll
-    for (int j = 0; j < FR; ++j) {
-      const int c = (wn * FR + j) * 16 + (lane >> 4) * 4;
-      if (c < clim) store4(p, (crow0 + r) * cols + c0 + c, sum[i][j]);
-    }
-  }
+  for (int i = 0; i < FR; ++i) store_fragments<FR>(o, p, sum[i], (wm * FR + i) * 16, wn * FR * 16, lane);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -349,109 +429,6 @@ __device__ __forceinline__ void bare_barrier() {
   __atomic_signal_fence(__ATOMIC_SEQ_CST);
 }
 
-// The value of the lane 8 further within the 16.
-__device__ __forceinline__ u32x4 rotate8(u32x4 v) {
-  u32x4 r;
-#pragma unroll
-  for (int q = 0; q < 4; ++q) r[q] = (unsigned)__builtin_amdgcn_mov_dpp((int)v[q], 0x128, 0xf, 0xf, true);
-  return r;
-}
-// 16 rows of which a lane holds 16 bytes of row lane % 16 in each of two 64-byte parts, a and b, to
-// 8 whole 128-byte pieces twice: put(row, part, v) gets 16 bytes of that row's part 0 or 1.
-template <typename F>
-__device__ __forceinline__ void store_row_halves(u32x4 a, u32x4 b, int lane, F&& put) {
-  const bool low = (lane & 8) == 0;
-  const u32x4 moved = rotate8(low ? b : a);
-  put(lane & 7, low ? 0 : 1, low ? a : moved);
-  put((lane & 7) + 8, low ? 0 : 1, low ? moved : b);
-}
-__device__ __forceinline__ unsigned pack_bf16(float a, float b) {
-  const bf16x2 v{(__bf16)a, (__bf16)b};
-  return __builtin_bit_cast(unsigned, v);
-}
-
-// The part of a tile of C that a wave stores. Stores go through a buffer descriptor that ends
-// with the tile's last row, and lanes past the last column aim behind it, so what lies outside
-// is dropped without a branch.
-struct OutTile {
-  __amdgpu_buffer_rsrc_t to;
-  int ld, clim;  // bytes of a row of C; columns that exist
-  static constexpr int kOutside = (int)0x80000000u;
-
-  // rows from row0 (mlim of them exist) and columns from c0 of out [.., cols]
-  __device__ __forceinline__ void set(const ProductArgs& p, size_t row0, int mlim, int c0, int clim_, int cols) {
-    const int size = p.out_bf16 ? 2 : 4;
-    ld = cols * size;
-    clim = clim_;
-    to = __builtin_amdgcn_make_buffer_rsrc(static_cast<char*>(p.out) + (row0 * cols + c0) * size, (short)0,
-                                           mlim * ld - c0 * size, kBufferWord3);
-  }
-  __device__ __forceinline__ int at(int r, int c, int size) const { return c < clim ? r * ld + c * size : kOutside; }
-};
-
-// 16 rows of C from r0 and NF * 16 columns from c0 of the tile. `v` is as the products leave it: 4
-// consecutive columns (from 4 (lane / 16)) of row lane % 16 in each 16-column fragment. Stored
-// like that, an instruction would write 64 bytes (fp32) or 32 (bf16) of each of 16 rows; lanes
-// first exchange parts so that it writes 128 bytes of each of 8 (2% of the large products' time).
-template <int NF>
-__device__ __forceinline__ void store_fragments(const OutTile& o, const ProductArgs& p, const f32x4 (&v)[NF], int r0,
-                                                int c0, int lane) {
-  if constexpr (NF % 2 == 0) {
-    if (!p.accumulate && !p.out_bf16) {
-#pragma unroll
-      for (int j = 0; j < NF; j += 2)
-        store_row_halves(__builtin_bit_cast(u32x4, v[j]), __builtin_bit_cast(u32x4, v[j + 1]), lane,
-                         [&](int r, int part, u32x4 x) __attribute__((always_inline)) {
-                           const int c = c0 + (j + part) * 16 + (lane >> 4) * 4;
-                           __builtin_amdgcn_raw_buffer_store_b128(x, o.to, o.at(r0 + r, c, 4), 0, 0);
-                         });
-      return;
-    }
-  }
-  if constexpr (NF % 4 == 0) {
-    if (!p.accumulate) {
-      u32x4 q[NF / 2];  // 8 columns of fragment j (even lane groups) or j + 1 (odd ones)
-#pragma unroll
-      for (int j = 0; j < NF; j += 2)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const auto s = __builtin_amdgcn_permlane16_swap(pack_bf16(v[j][2 * h], v[j][2 * h + 1]),
-                                                          pack_bf16(v[j + 1][2 * h], v[j + 1][2 * h + 1]), false, false);
-          q[j / 2][h] = s[0];
-          q[j / 2][2 + h] = s[1];
-        }
-#pragma unroll
-      for (int j = 0; j < NF / 2; j += 2)
-        store_row_halves(q[j], q[j + 1], lane, [&](int r, int part, u32x4 x) __attribute__((always_inline)) {
-          const int g = lane >> 4;
-          const int c = c0 + (j + part) * 32 + (g & 1) * 16 + (g >> 1) * 8;
-          __builtin_amdgcn_raw_buffer_store_b128(x, o.to, o.at(r0 + r, c, 2), 0, 0);
-        });
-      return;
-    }
-  }
-  const int r = r0 + (lane & 15);
-#pragma unroll
-  for (int j = 0; j < NF; ++j) {
-    const int c = c0 + j * 16 + (lane >> 4) * 4;
-    f32x4 x = v[j];
-    if (p.out_bf16) {
-      const int at = o.at(r, c, 2);
-      if (p.accumulate) {
-        const u32x2 old = __builtin_amdgcn_raw_buffer_load_b64(o.to, at, 0, 0);
-        x[0] += __uint_as_float(old[0] << 16);
-        x[1] += __uint_as_float(old[0] & 0xffff0000u);
-        x[2] += __uint_as_float(old[1] << 16);
-        x[3] += __uint_as_float(old[1] & 0xffff0000u);
-      }
-      __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])}, o.to, at, 0, 0);
-    } else {
-      const int at = o.at(r, c, 4);
-      if (p.accumulate) x += __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(o.to, at, 0, 0));
-      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), o.to, at, 0, 0);
-    }
-  }
-}
 // A workgroup of WGM x WGN waves computes a tile of C, each wave WM x WN of it with
 // v_mfma_f32_16x16x32_bf16; steps of DK go through a ring of RING slots in LDS. While a
 // slice's products run, the fragments of the next slice are read (B into the other of two
@@ -605,28 +582,31 @@ hipError_t launch_product(const GroupedGemmArgs& a, hipStream_t stream) {
     return hipGetLastError();
   }
   // Which tiles, from the sizes alone (the host does not know the offsets). Measured at 64 experts of
-  // 2048 x 4096, rows spread evenly and by Zipf 1.2 (us, even rows):
-  //   rows per expert            8     16     32     64    128    256    512
-  //   forward  32 x 64 tiles   173    178
-  //            64 x 128        184    187    192    204    273    448
-  //            256 x 256       247    243    245    254    268    298    491
-  //   dgrad 2  32 x 128        326    335
-  //            64 x 128        329    338    352    391    565    945
-  //            256 x 256       376    378    384    390    420    534    980
-  //   wgrad    128 x 128       563           587    590    639    865   1168
-  //            256 x 256       522           535    551    611    734    908
-  // (dgrad with skewed rows: 64 x 128 wins from 16 rows on). Large tiles are wasted on a width that
-  // fills less than one of them.
+  // 2048 x 4096, rows spread evenly (us):
+  //   rows per expert             8     16     32     64     96    128    256    512
+  //   forward  32 x 64 tiles    163    178
+  //            64 x 128         184    187    192    204           273    448    833
+  //            256 x 256        247    243    245    254           268    298    491
+  //   dgrad 2  32 x 128         325    335
+  //            64 x 128         329    338    352    391           565    945   1804
+  //            256 x 256        376    378    384    390           420    534    980
+  //   wgrad    128 x 128, fp32  334           354    365           424    605    961
+  //            256 x 256, fp32  420           433    437           474    557    781
+  //            128 x 128, bf16                237    249    305    316    573    859
+  //            256 x 256, bf16                233    239    273    284    412    725
+  // (With rows dealt by Zipf 1.2 the borders are the same or a little lower. With 1 row per expert a
+  // bf16 weight gradient takes 186 us in tiles of 128, 204 in tiles of 256.) Large tiles are wasted
+  // on a width that fills less than one of them.
   const long long mean = a.rows / a.E;
   if constexpr (P == kWgrad) {
-    if (a.N > 128 && a.K > 128) return launch_tiles<P, 128, 64, 2, 4, 64, 2, false, true>(a, p, stream);
+    if (mean >= (a.out_bf16 ? 16 : 160) && a.N > 128 && a.K > 128) return launch_tiles<P, 128, 64, 2, 4, 64, 2, false, true>(a, p, stream);
     return launch_tiles<P, 64, 64, 2, 2, 64, 2, false, false>(a, p, stream);
   } else {
     if (mean >= 96 && (P == kForward ? a.N : a.K) > 128)
       return launch_tiles<P, 128, 64, 2, 4, 64, 2, false, true>(a, p, stream);
     if (mean >= 12) return launch_tiles<P, 32, 64, 2, 2, 64, 3, true, false>(a, p, stream);
-    if constexpr (P == kForward) return launch_tiles<P, 32, 16, 1, 4, 128, 4, true, false>(a, p, stream);
-    return launch_tiles<P, 32, 32, 1, 4, 64, 4, true, false>(a, p, stream);
+    if constexpr (P == kForward) return launch_tiles<P, 32, 16, 1, 4, 128, 3, true, false>(a, p, stream);
+    return launch_tiles<P, 32, 32, 1, 4, 64, 3, true, false>(a, p, stream);
   }
 }
 
