@@ -23,8 +23,8 @@ namespace {
 // ---------------------------------------------------------------------------------------
 // fp32: tiles staged through registers
 // ---------------------------------------------------------------------------------------
-// A workgroup of 4 waves (2 x 2) computes a TM x TM tile of C; the contraction goes in steps of
-// 32. Both operands lie in LDS in their memory order: along operands [m][32 + 4],
+// A workgroup of 4 waves computes a tile of C, each wave FM x FN fragments of 16 x 16; the contraction
+// goes in steps of 32. Both operands lie in LDS in their memory order: along operands [m][32 + 4],
 // across operands [32][m + 4]; the padding of 4 floats puts the 16 rows (or 4 row groups) of a
 // fragment read on distinct banks. v_mfma_f32_16x16x4_f32 takes one contraction element per
 // lane (row or column lane % 16, element lane / 16); lane group g takes elements 4g .. 4g + 3
@@ -35,7 +35,6 @@ namespace {
 // for the weight gradient. Tiles of 128 measured slower at every size (693, 1380 and 736 us).
 constexpr int kStep = 32;
 constexpr int kPad = 4;
-constexpr int kF32Tile = 64;
 
 struct ProductArgs {
   const void *a, *b, *a2, *b2;  // a2, b2: second pair of operands (dgrad), or null
@@ -200,7 +199,8 @@ __device__ __forceinline__ bool tile_at(const ProductArgs& p, int TM, int TN, Ti
 // number. What lies outside reads as zero.
 template <bool ACROSS, int TM>
 struct Stage {
-  static constexpr int NCH = TM * kStep / 4 / 256;  // 4-element chunks per thread
+  static constexpr int kAll = TM * kStep / 4;          // 4-element chunks
+  static constexpr int NCH = (kAll + 255) / 256;       // per thread
   float4 c[NCH];
   __device__ __forceinline__ static void at(int i, int& outer, int& inner) {
     const int q = threadIdx.x + i * 256;
@@ -213,7 +213,8 @@ struct Stage {
     for (int i = 0; i < NCH; ++i) {
       int o, n;
       at(i, o, n);
-      const bool ok = ACROSS ? (k0 + o < kdim && n < lim) : (o < lim && k0 + n < kdim);
+      const bool ok = (kAll % 256 == 0 || (int)threadIdx.x + i * 256 < kAll) &&
+                      (ACROSS ? (k0 + o < kdim && n < lim) : (o < lim && k0 + n < kdim));
       const size_t e = ACROSS ? (size_t)(k0 + o) * ld + n : (size_t)o * ld + k0 + n;
       c[i] = ok ? *reinterpret_cast<const float4*>(base + e) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
@@ -224,7 +225,7 @@ struct Stage {
     for (int i = 0; i < NCH; ++i) {
       int o, n;
       at(i, o, n);
-      *reinterpret_cast<float4*>(lds + o * row + n) = c[i];
+      if (kAll % 256 == 0 || (int)threadIdx.x + i * 256 < kAll) *reinterpret_cast<float4*>(lds + o * row + n) = c[i];
     }
   }
 };
@@ -243,19 +244,19 @@ __device__ __forceinline__ f32x4 fragment(const float* lds, int m, int k) {
 template <bool ACROSS, int TM>
 constexpr int stage_floats() { return ACROSS ? kStep * (TM + kPad) : TM * (kStep + kPad); }
 
-template <GroupedProduct P, int TM>
+template <GroupedProduct P, int FM, int FN, int WGM>
 __global__ __launch_bounds__(256) void f32_kernel(ProductArgs p) {
   constexpr bool AX = P == kWgrad, BX = P != kForward;
-  constexpr int FR = TM / 32;  // 16-wide fragments per wave and side
+  constexpr int WGN = 4 / WGM, TM = 16 * FM * WGM, TN = 16 * FN * WGN;
   __shared__ __align__(16) float la[stage_floats<AX, TM>()];
-  __shared__ __align__(16) float lb[stage_floats<BX, TM>()];
+  __shared__ __align__(16) float lb[stage_floats<BX, TN>()];
   TileAt t;
-  if (!tile_at<P, false>(p, TM, TM, t)) return;
+  if (!tile_at<P, false>(p, TM, TN, t)) return;
   const int e = t.e, ra = t.ra, m0 = t.m0, c0 = t.c0, mlim = t.mlim, clim = t.clim, kdim = t.kdim;
   const int cols = P == kForward ? p.N : p.K;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave & 1, wn = wave >> 1;
+  const int wm = wave % WGM, wn = wave / WGM;
   const int lda = P == kForward ? p.K : p.N;
   const size_t wbase = (size_t)e * p.N * p.K;
   const size_t a_at = P == kWgrad ? (size_t)ra * p.N + m0 : (size_t)(ra + m0) * lda;
@@ -265,16 +266,16 @@ __global__ __launch_bounds__(256) void f32_kernel(ProductArgs p) {
   // Sums in two levels: `acc` over kRun steps, `sum` over those. One chain of K / 4 additions was
   // twice as far from the 64-bit result at K = 4096.
   constexpr int kRun = 8;
-  f32x4 acc[FR][FR], sum[FR][FR];
+  f32x4 acc[FM][FN], sum[FM][FN];
 #pragma unroll
-  for (int i = 0; i < FR; ++i)
+  for (int i = 0; i < FM; ++i)
 #pragma unroll
-    for (int j = 0; j < FR; ++j) acc[i][j] = sum[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < FN; ++j) acc[i][j] = sum[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   const int steps1 = (kdim + kStep - 1) / kStep;
   const int steps = (P == kDgrad && p.a2) ? 2 * steps1 : steps1;
   Stage<AX, TM> sa;
-  Stage<BX, TM> sb;
+  Stage<BX, TN> sb;
   auto load = [&](int st) __attribute__((always_inline)) {
     const bool second = st >= steps1;
     const int k0 = (second ? st - steps1 : st) * kStep;
@@ -291,24 +292,24 @@ __global__ __launch_bounds__(256) void f32_kernel(ProductArgs p) {
 #pragma unroll
     for (int s = 0; s < kStep / 16; ++s) {
       const int k = s * 16 + (lane >> 4) * 4;
-      f32x4 fa[FR], fb[FR];
+      f32x4 fa[FM], fb[FN];
 #pragma unroll
-      for (int i = 0; i < FR; ++i) fa[i] = fragment<AX, TM>(la, (wm * FR + i) * 16 + (lane & 15), k);
+      for (int i = 0; i < FM; ++i) fa[i] = fragment<AX, TM>(la, (wm * FM + i) * 16 + (lane & 15), k);
 #pragma unroll
-      for (int i = 0; i < FR; ++i) fb[i] = fragment<BX, TM>(lb, (wn * FR + i) * 16 + (lane & 15), k);
+      for (int j = 0; j < FN; ++j) fb[j] = fragment<BX, TN>(lb, (wn * FN + j) * 16 + (lane & 15), k);
 #pragma unroll
       for (int q = 0; q < 4; ++q)
 #pragma unroll
-        for (int i = 0; i < FR; ++i)
+        for (int i = 0; i < FM; ++i)
 #pragma unroll
-          for (int j = 0; j < FR; ++j)
+          for (int j = 0; j < FN; ++j)
             acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(fb[j][q], fa[i][q], acc[i][j], 0, 0, 0);
     }
     if (st % kRun == kRun - 1 || st == steps - 1) {
 #pragma unroll
-      for (int i = 0; i < FR; ++i)
+      for (int i = 0; i < FM; ++i)
 #pragma unroll
-        for (int j = 0; j < FR; ++j) {
+        for (int j = 0; j < FN; ++j) {
           sum[i][j] += acc[i][j];
           acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
@@ -317,7 +318,7 @@ __global__ __launch_bounds__(256) void f32_kernel(ProductArgs p) {
   OutTile o;
   o.set(p, P == kWgrad ? (size_t)e * p.N + m0 : (size_t)ra + m0, mlim, c0, clim, cols);
 #pragma unroll
-  for (int i = 0; i < FR; ++i) store_fragments<FR>(o, p, sum[i], (wm * FR + i) * 16, wn * FR * 16, lane);
+  for (int i = 0; i < FM; ++i) store_fragments<FN>(o, p, sum[i], (wm * FM + i) * 16, wn * FN * 16, lane);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -572,14 +573,23 @@ hipError_t launch_tiles(const GroupedGemmArgs& a, const ProductArgs& p, hipStrea
   return hipGetLastError();
 }
 
+template <GroupedProduct P, int FM, int FN, int WGM>
+hipError_t launch_f32(const GroupedGemmArgs& a, const ProductArgs& p, hipStream_t stream) {
+  const long long grid = xcd_grid(tile_items(P, a, 16 * FM * WGM, 16 * FN * (4 / WGM)));
+  f32_kernel<P, FM, FN, WGM><<<(unsigned)grid, 256, 0, stream>>>(p);
+  return hipGetLastError();
+}
+
 template <GroupedProduct P>
 hipError_t launch_product(const GroupedGemmArgs& a, hipStream_t stream) {
   const ProductArgs p{a.a, a.b, a.a2, a.b2, a.out, a.offsets, a.rows, a.E, a.N, a.K,
                       a.out_bf16 ? 1 : 0, a.accumulate ? 1 : 0};
   if (!a.bf16) {
-    const long long grid = xcd_grid(tile_items(P, a, kF32Tile, kF32Tile));
-    f32_kernel<P, kF32Tile><<<(unsigned)grid, 256, 0, stream>>>(p);
-    return hipGetLastError();
+    // Few rows leave most of a 64-row tile's products empty: at 64 experts of 1024 x 2048, even rows,
+    // tiles of 16 x 64 against 64 x 64 took (forward) 124 and 166 us at 1 row per expert, 128 and
+    // 165 at 32, 235 and 180 at 64.
+    if (P != kWgrad && a.rows / a.E < 48) return launch_f32<P, 1, 1, 1>(a, p, stream);
+    return launch_f32<P, 2, 2, 2>(a, p, stream);
   }
   // Which tiles, from the sizes alone (the host does not know the offsets). Measured at 64 experts of
   // 2048 x 4096, rows spread evenly (us):
@@ -613,7 +623,7 @@ hipError_t launch_product(const GroupedGemmArgs& a, hipStream_t stream) {
 }  // namespace
 
 bool grouped_gemm_fits(const GroupedGemmArgs& a, GroupedProduct kind) {
-  return xcd_grid(tile_items(kind, a, 32, 64)) <= 0x7fffffffLL;  // the smallest tiles
+  return xcd_grid(tile_items(kind, a, 16, 64)) <= 0x7fffffffLL;  // the smallest tiles
 }
 
 hipError_t launch_grouped_gemm(const GroupedGemmArgs& a, GroupedProduct kind, hipStream_t stream) {
