@@ -24,19 +24,20 @@ __device__ __forceinline__ int rows_in_use(const int32_t* offsets, int E, int ro
   return n < 0 ? 0 : (n > rows ? rows : n);
 }
 
-// Workgroup b's item. The hardware deals workgroups to the 8 XCDs in turn (workgroup b runs on
-// XCD b % 8) and each XCD has an L2 of its own, so runs of kXcdRun consecutive items, which
-// share operands, go to one XCD, and the runs go round the XCDs.
-constexpr int kXcdRun = 32;
-__device__ __forceinline__ long long xcd_item(unsigned b) {
-  const unsigned x = b & 7, i = b >> 3;
-  return ((long long)(i / kXcdRun) * 8 + x) * kXcdRun + i % kXcdRun;
+// Workgroup b's item of `items`, or -1. The hardware deals workgroups to the 8 XCDs in turn
+// (workgroup b runs on XCD b % 8) and each XCD has an L2 of its own: every 256 workgroups take 256
+// consecutive items, and each XCD a run of 32 of them, which share operands; a last, smaller round
+// is cut into 8 runs as well, so that it keeps every XCD busy.
+constexpr int kRound = 256;
+__device__ __forceinline__ int xcd_item(unsigned b, unsigned items) {
+  const unsigned base = b & ~(kRound - 1u);
+  if (base >= items) return -1;
+  const unsigned n = min((unsigned)kRound, items - base), run = (n + 7) / 8;
+  const unsigned i = (b - base) >> 3, at = (b & 7) * run + i;
+  return i < run && at < n ? (int)(base + at) : -1;
 }
-// Grid that covers `items` items under that map.
-inline long long xcd_grid(long long items) {
-  const long long round = 8 * kXcdRun;
-  return (items + round - 1) / round * round;
-}
+// Workgroups that meet all of `items` under that map.
+inline long long xcd_grid(long long items) { return (items + kRound - 1) / kRound * kRound; }
 
 // Tile pair of the i-th of mtiles * NT tiles: groups of kGroupM row tiles walk the column tiles
 // together, so that the tiles in flight on one XCD share both operands.
@@ -50,11 +51,10 @@ __device__ __forceinline__ void tile_pair(int i, int mtiles, int NT, int& mt, in
 }
 
 // Row tiles of TM rows, expert by expert; each of an expert's row tiles meets NT column tiles.
-// Finds item's expert e, its rows [a, b) and the tile pair (mt, nt) within the expert; false
-// past the last item.
+// Finds this workgroup's item: its expert e, the expert's rows [a, b) and the tile pair (mt, nt)
+// within the expert; false if there is none.
 __device__ __forceinline__ bool find_row_tile(const int32_t* offsets, int E, int rows, int TM,
-                                              int NT, long long item, int& e, int& a, int& b,
-                                              int& mt, int& nt) {
+                                              int NT, int& e, int& a, int& b, int& mt, int& nt) {
   const int lane = threadIdx.x & 63;
   const int per = (E + 63) / 64;  // consecutive experts per lane
   int mine = 0;
@@ -72,11 +72,10 @@ __device__ __forceinline__ bool find_row_tile(const int32_t* offsets, int E, int
     const int v = __shfl_up(incl, d);
     if (lane >= d) incl += v;
   }
-  const long long q64 = item / NT;
-  const int total = __builtin_amdgcn_readlane(incl, 63);
-  if (q64 >= total) return false;
-  const int q = (int)q64;
-  const unsigned long long past = __ballot(incl > q);  // never empty: q < total
+  const int item = xcd_item(blockIdx.x, (unsigned)__builtin_amdgcn_readlane(incl, 63) * (unsigned)NT);
+  if (item < 0) return false;
+  const int q = item / NT;
+  const unsigned long long past = __ballot(incl > q);  // never empty: q < all tiles
   const int owner = __ffsll(past) - 1;
   int pre = __builtin_amdgcn_readlane(incl - mine, owner);
   // the owner's experts, read by every lane (uniform addresses)
@@ -93,7 +92,7 @@ __device__ __forceinline__ bool find_row_tile(const int32_t* offsets, int E, int
   b = __builtin_amdgcn_readfirstlane(b);
   pre = __builtin_amdgcn_readfirstlane(pre);
   mtiles = __builtin_amdgcn_readfirstlane(mtiles);
-  tile_pair((int)(item - (long long)pre * NT), mtiles, NT, mt, nt);
+  tile_pair(item - pre * NT, mtiles, NT, mt, nt);
   return true;
 }
 

@@ -13,6 +13,8 @@
 //   forward  A = x along K,   B = W along K
 //   dgrad    A = dy along N,  B = W across N
 //   wgrad    A = dy across r, B = x across r
+#include <cmath>
+
 #include "grouped.h"
 #include "lds_tiles.h"
 
@@ -159,22 +161,22 @@ struct TileAt {
 // which read the same B, take about the same time.
 template <GroupedProduct P, bool DEAL>
 __device__ __forceinline__ bool tile_at(const ProductArgs& p, int TM, int TN, TileAt& t) {
-  const long long item = xcd_item(blockIdx.x);
   const int cols = P == kForward ? p.N : p.K;
   const int CT = (cols + TN - 1) / TN;
   int mt, nt;
   if constexpr (P == kWgrad) {
-    const long long per = (long long)((p.N + TM - 1) / TM) * CT;
-    if (item >= p.E * per) return false;
+    const int per = (p.N + TM - 1) / TM * CT;
+    const int item = xcd_item(blockIdx.x, (unsigned)p.E * (unsigned)per);
+    if (item < 0) return false;
     // Experts in their order: starting with those of the most rows cost 3 to 12%, whichever way the
     // rows were dealt (64 experts, Zipf 1.2: 444 against 396 us). Side by side, tiles of different
     // lengths do not all store at the same time.
-    t.e = (int)(item / per);
+    t.e = item / per;
     group_rows(p.offsets, t.e, p.rows, t.ra, t.rb);
-    tile_pair((int)(item % per), (p.N + TM - 1) / TM, CT, mt, nt);
+    tile_pair(item % per, (p.N + TM - 1) / TM, CT, mt, nt);
     if (t.ra == t.rb && p.accumulate) return false;
   } else {
-    if (!find_row_tile(p.offsets, p.E, p.rows, TM, CT, item, t.e, t.ra, t.rb, mt, nt)) return false;
+    if (!find_row_tile(p.offsets, p.E, p.rows, TM, CT, t.e, t.ra, t.rb, mt, nt)) return false;
   }
   const int n = P == kWgrad ? p.N : t.rb - t.ra;  // C's rows
   t.m0 = mt * TM;
@@ -580,8 +582,29 @@ hipError_t launch_f32(const GroupedGemmArgs& a, const ProductArgs& p, hipStream_
   return hipGetLastError();
 }
 
+// Time, per contraction step of 64 (us), of TM x TN tiles over the CUs, `fit` to each at a time: `full`
+// where the CUs are filled, `alone` for a last round with at most one tile to a CU. With several
+// experts, each one's last row tile is taken to be half full. The times are from products of 512
+// to 8192 rows over 1 to 16 experts (forward, 1024 rows of 2048 x 7168 for one expert: 136 us in
+// tiles of 256, 78 of 128, 59 of 64 x 128; 4096 rows of 4096 x 1024 for 8 experts: 33, 43 and 55).
+struct TileCost {
+  int TM, TN, fit;
+  double alone, full;
+};
+constexpr TileCost kBig{256, 256, 1, 1.3, 1.3}, kMid{128, 128, 2, 0.7, 1.05}, kSmall{64, 128, 2, 0.48, 0.75};
+
+double step_time(GroupedProduct kind, const GroupedGemmArgs& a, const TileCost& c, int cus) {
+  const double active = a.E < a.rows ? a.E : a.rows;
+  double tiles = kind == kWgrad ? a.E * std::ceil(a.N / (double)c.TM)
+                 : a.E == 1     ? std::ceil(a.rows / (double)c.TM)
+                                : std::fmax(a.rows / (double)c.TM + 0.5 * active, active);
+  tiles *= std::ceil((kind == kForward ? a.N : a.K) / (double)c.TN);
+  const double slots = (double)cus * c.fit, whole = std::floor(tiles / slots), left = tiles - whole * slots;
+  return whole * c.full + (left == 0 ? 0 : left <= cus ? c.alone : c.full);
+}
+
 template <GroupedProduct P>
-hipError_t launch_product(const GroupedGemmArgs& a, hipStream_t stream) {
+hipError_t launch_product(const GroupedGemmArgs& a, int cus, hipStream_t stream) {
   const ProductArgs p{a.a, a.b, a.a2, a.b2, a.out, a.offsets, a.rows, a.E, a.N, a.K,
                       a.out_bf16 ? 1 : 0, a.accumulate ? 1 : 0};
   if (!a.bf16) {
@@ -596,24 +619,34 @@ hipError_t launch_product(const GroupedGemmArgs& a, hipStream_t stream) {
   //   rows per expert             8     16     32     64     96    128    256    512
   //   forward  32 x 64 tiles    163    178
   //            64 x 128         184    187    192    204           273    448    833
+  //            128 x 128        237    239    239    249           262    362    650
   //            256 x 256        247    243    245    254           268    298    491
   //   dgrad 2  32 x 128         325    335
   //            64 x 128         329    338    352    391           565    945   1804
+  //            128 x 128        362    365    372    394           433    714   1321
   //            256 x 256        376    378    384    390           420    534    980
   //   wgrad    128 x 128, fp32  334           354    365           424    605    961
   //            256 x 256, fp32  420           433    437           474    557    781
   //            128 x 128, bf16                237    249    305    316    573    859
   //            256 x 256, bf16                233    239    273    284    412    725
-  // (With rows dealt by Zipf 1.2 the borders are the same or a little lower. With 1 row per expert a
-  // bf16 weight gradient takes 186 us in tiles of 128, 204 in tiles of 256.) Large tiles are wasted
-  // on a width that fills less than one of them.
+  // With rows dealt by Zipf 1.2 or 0.6 the borders are the same or a little lower, but forward tiles of
+  // 128 stay ahead to about 192 rows (128 per expert, Zipf 0.6: 257 us against 311). With 1 row per
+  // expert a bf16 weight gradient takes 186 us in tiles of 128, 204 in tiles of 256. Large tiles
+  // are wasted on a width that fills less than one of them, and where there are fewer of them than
+  // CUs (step_time).
   const long long mean = a.rows / a.E;
+  const double big = step_time(P, a, kBig, cus), mid = step_time(P, a, kMid, cus);
   if constexpr (P == kWgrad) {
-    if (mean >= (a.out_bf16 ? 16 : 160) && a.N > 128 && a.K > 128) return launch_tiles<P, 128, 64, 2, 4, 64, 2, false, true>(a, p, stream);
+    if (mean >= (a.out_bf16 ? 16 : 160) && a.N > 128 && a.K > 128 && big <= mid)
+      return launch_tiles<P, 128, 64, 2, 4, 64, 2, false, true>(a, p, stream);
     return launch_tiles<P, 64, 64, 2, 2, 64, 2, false, false>(a, p, stream);
   } else {
-    if (mean >= 96 && (P == kForward ? a.N : a.K) > 128)
-      return launch_tiles<P, 128, 64, 2, 4, 64, 2, false, true>(a, p, stream);
+    if (mean >= 96) {
+      const double small = step_time(P, a, kSmall, cus);
+      if (mean >= (P == kForward ? 192 : 96) && (P == kForward ? a.N : a.K) > 128 && big <= mid && big <= small)
+        return launch_tiles<P, 128, 64, 2, 4, 64, 2, false, true>(a, p, stream);
+      if (mid <= small) return launch_tiles<P, 64, 64, 2, 2, 64, 2, true, false>(a, p, stream);
+    }
     if (mean >= 12) return launch_tiles<P, 32, 64, 2, 2, 64, 3, true, false>(a, p, stream);
     if constexpr (P == kForward) return launch_tiles<P, 32, 16, 1, 4, 128, 3, true, false>(a, p, stream);
     return launch_tiles<P, 32, 32, 1, 4, 64, 3, true, false>(a, p, stream);
@@ -627,10 +660,13 @@ bool grouped_gemm_fits(const GroupedGemmArgs& a, GroupedProduct kind) {
 }
 
 hipError_t launch_grouped_gemm(const GroupedGemmArgs& a, GroupedProduct kind, hipStream_t stream) {
+  DeviceInfo dev;
+  const hipError_t e = device_info(&dev);
+  if (e != hipSuccess) return e;
   switch (kind) {
-    case kForward: return launch_product<kForward>(a, stream);
-    case kDgrad: return launch_product<kDgrad>(a, stream);
-    case kWgrad: return launch_product<kWgrad>(a, stream);
+    case kForward: return launch_product<kForward>(a, dev.num_cus, stream);
+    case kDgrad: return launch_product<kDgrad>(a, dev.num_cus, stream);
+    case kWgrad: return launch_product<kWgrad>(a, dev.num_cus, stream);
   }
   return hipErrorInvalidValue;
 }
