@@ -251,3 +251,77 @@ def test_same_bits_every_call_and_on_another_stream(dev):
     for o in outs[1:]:
         for a, b in zip(o, outs[0]):
             assert torch.equal(a, b)
+
+
+# Sizes with enough rows and tiles for each kind of tile that the library chooses among (see the rule in
+# grouped_gemm.hip): 256 x 256, 128 x 128, 64 x 128 and the few-row tiles, with partial tiles on every side
+@pytest.mark.parametrize("counts,N,K", [
+    ([1500, 0, 17, 2579], 2056, 520),           # 256 x 256 forward
+    ([1300, 900, 0, 1900], 520, 2056),          # 256 x 256 input gradient
+    ([700, 5, 0, 1200, 300, 64, 1, 800], 1800, 2056),   # 256 x 256 weight gradient
+    ([150] * 20 + [0, 3, 290], 1032, 1160),     # 128 x 128
+    ([30, 0, 55, 70] * 8, 392, 1160),           # 64 x 128
+    ([3, 1, 0, 14] * 30, 1544, 264),            # few rows
+], ids=["large-forward", "large-dgrad", "large-wgrad", "middle", "small", "few"])
+@pytest.mark.parametrize("out", [F32, BF])
+def test_every_tile_size_exact(dev, counts, N, K, out):
+    run_all(counts, 3, N, K, BF, out, dev, seed=12)
+
+
+def test_large_tiles_of_normal_values(dev):
+    run_all([1500, 0, 17, 2579], 3, 2056, 520, BF, BF, dev, seed=13, make=normal, exact=False)
+    run_all([1300, 900, 0, 1900], 0, 520, 2056, BF, F32, dev, seed=14, make=normal, exact=False)
+
+
+@pytest.mark.parametrize("counts,N,K", [([1500, 0, 17, 2579], 2056, 520), ([1300, 900, 0, 1900], 520, 2056),
+                                        ([150] * 20 + [0, 3, 290], 264, 328), ([3, 1, 0, 14] * 30, 1544, 264)])
+def test_products_captured_and_replayed(dev, counts, N, K):
+    """Each product in a graph: replays with other inputs, rows dealt anew on the device (the graph holds no
+    counts), other eager work in between; every replay against the eager call."""
+    n = sum(counts)
+    t = inputs(counts, 0, N, K, BF, dev, seed=15, make=normal)
+    for w in ("w", "w2"):
+        t[w].nan_to_num_(0.5)
+    E = len(counts)
+    out = dict(y=torch.empty((n, N), device=dev), dx=torch.empty((n, K), dtype=BF, device=dev),
+               dw=torch.empty((E, N, K), dtype=BF, device=dev))
+
+    def run(o, stream=None):
+        moe.moe_grouped_gemm(t["x"], t["offsets"], t["w"], o["y"])
+        moe.moe_grouped_gemm_dgrad(t["dy"], t["offsets"], t["w"], o["dx"], dy2=t["dy2"], w2=t["w2"])
+        moe.moe_grouped_gemm_wgrad(t["dy"], t["x"], t["offsets"], o["dw"])
+    run(out)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run(out)
+    order = list(counts)
+    for rep in range(4):
+        order = order[1:] + order[:1]
+        t["offsets"].copy_(ref.offsets_of(order, dev))
+        t["x"].copy_(normal((n, K), 200 + rep, dev))
+        for o in out.values():
+            o.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        eager = {k: torch.full_like(v, float("nan")) for k, v in out.items()}
+        run(eager)
+        torch.cuda.synchronize()
+        for k in out:
+            assert torch.equal(out[k], eager[k]), (rep, k)
+
+
+def test_offsets_that_are_wrong_stay_in_bounds(dev):
+    """Offsets that no permutation writes (falling, negative, past the rows) give unspecified results, but
+    nothing is read or written outside the buffers."""
+    N, K, rows = 136, 264, 300
+    t = inputs([100, 100, 100], 0, N, K, BF, dev, seed=16)
+    for bad in ([0, 250, 100, 300], [-5, 900, 20, 7], [2 ** 31 - 1] * 4, [300, 200, 100, 0]):
+        off = torch.tensor(bad, dtype=torch.int32, device=dev)
+        for shape, call in (((rows, N), lambda o: moe.moe_grouped_gemm(t["x"], off, t["w"], o)),
+                            ((rows, K), lambda o: moe.moe_grouped_gemm_dgrad(t["dy"], off, t["w"], o)),
+                            ((3, N, K), lambda o: moe.moe_grouped_gemm_wgrad(t["dy"], t["x"], off, o))):
+            o, whole = ref.guarded(shape, F32, dev)
+            call(o)
+            torch.cuda.synchronize()
+            assert ref.guards_intact(whole, o.numel())
