@@ -322,10 +322,11 @@ moe_status_t moe_layer_capped(const float* logits, const void* x, moe_dtype_t ac
  * pass needs of the forward pass can be held in 8 bits (moe_checkpoint_pack, moe_swiglu).
  *
  * In all of them d, d_ff, N and K are multiples of 8 and at most 2^20 (MOE_ERR_UNSUPPORTED /
- * MOE_ERR_INVALID_ARG otherwise), element counts may pass 2^31, and a size whose kernels would
- * need more than 2^31 - 1 workgroups gives MOE_ERR_UNSUPPORTED. Rows at or past offsets[E]
- * (kept rows after moe_permute_capped) are neither read nor written. Results in MOE_BF16 are
- * the fp32 result rounded once, to nearest even. None of these calls needs a workspace.
+ * MOE_ERR_INVALID_ARG otherwise), element counts may pass 2^32, and a size whose kernels would
+ * need more than 2^32 threads gives MOE_ERR_UNSUPPORTED (rows * k or tiles in the order of
+ * 10^7). Rows at or past offsets[E] (kept rows after moe_permute_capped) are neither read nor
+ * written. Results in MOE_BF16 are the fp32 result rounded once, to nearest even. None of these
+ * calls needs a workspace.
  */
 
 /*
@@ -420,6 +421,8 @@ moe_status_t moe_swiglu(const void* g, const void* u, moe_dtype_t dtype, const i
 /*
  * moe_swiglu_backward - with s = 1 / (1 + e^-g):
  *     du = dh g s,   dg = dh u s (1 + g (1 - s)),   h = g s u
+ *   computed in fp32 (with dtype MOE_BF16, results under 2^-120 may come out as 0, here and in
+ *   moe_swiglu: g around -87 and below).
  *   dh       [rows, d_ff] in dtype (MOE_BF16 or MOE_F32); dg, du out and h out (or NULL), same
  *            shape and dtype. h is the forward result again, for the down projection's weight
  *            gradient.

@@ -183,8 +183,6 @@ moe_status_t check_combine(const float* y_sorted, const int32_t* f2s, const floa
 }
 
 // ---- training ----
-constexpr long long kMaxGrid = 0x7fffffffLL;
-
 bool float_dtype(moe_dtype_t t) { return t == MOE_F32 || t == MOE_BF16; }
 // MOE_OK for the two formats of activations and gradients, else why not
 moe_status_t check_float_dtype(moe_dtype_t t) {
@@ -495,7 +493,7 @@ moe_status_t moe_checkpoint_pack(const void* x, moe_dtype_t x_dtype, int rows, i
   const long long n = (long long)rows * d;
   if (!ok_ptr(x, n, 16) || !ok_ptr(codes, n, 16) || !ok_ptr(scales, rows * held_groups(d), 4))
     return MOE_ERR_INVALID_ARG;
-  if (moe::row_kernel_grid(rows, d) > kMaxGrid) return MOE_ERR_UNSUPPORTED;
+  if (moe::row_kernel_grid(rows, d) > moe::kMaxWorkgroups) return MOE_ERR_UNSUPPORTED;
   return hip_status(moe::launch_pack(x, x_dtype == MOE_BF16, rows, d, codes, scales,
                                      static_cast<hipStream_t>(stream)));
 }
@@ -512,7 +510,7 @@ moe_status_t moe_checkpoint_unpack(const void* codes, const float* scales, int T
   if (!ok_ptr(codes, n, 16) || !ok_ptr(scales, T * held_groups(d), 4) || !ok_ptr(out, n * k, 16) ||
       !aligned(flat_to_sorted, 4))
     return MOE_ERR_INVALID_ARG;
-  if (moe::row_kernel_grid(T, d) > kMaxGrid) return MOE_ERR_UNSUPPORTED;
+  if (moe::row_kernel_grid(T, d) > moe::kMaxWorkgroups) return MOE_ERR_UNSUPPORTED;
   return hip_status(moe::launch_unpack(codes, scales, T, k, d, flat_to_sorted, out, out_dtype == MOE_BF16,
                                        static_cast<hipStream_t>(stream)));
 }
@@ -530,7 +528,7 @@ moe_status_t moe_swiglu(const void* g, const void* u, moe_dtype_t dtype, const i
   if ((g_codes || g_scales || u_codes || u_scales) &&
       (!ok_ptr(g_codes, n, 16) || !ok_ptr(u_codes, n, 16) || !ok_ptr(g_scales, ng, 4) || !ok_ptr(u_scales, ng, 4)))
     return MOE_ERR_INVALID_ARG;
-  if (moe::row_kernel_grid(rows, d_ff) > kMaxGrid) return MOE_ERR_UNSUPPORTED;
+  if (moe::row_kernel_grid(rows, d_ff) > moe::kMaxWorkgroups) return MOE_ERR_UNSUPPORTED;
   return hip_status(moe::launch_swiglu(g, u, dtype == MOE_BF16, offsets, E, rows, d_ff, h, g_codes, g_scales,
                                        u_codes, u_scales, static_cast<hipStream_t>(stream)));
 }
@@ -555,7 +553,7 @@ moe_status_t moe_swiglu_backward(const void* dh, moe_dtype_t dtype, const void* 
     return MOE_ERR_INVALID_ARG;
   if (held ? (!ok_ptr(g_scales, ng, 4) || !ok_ptr(u_scales, ng, 4)) : (g_scales || u_scales))
     return MOE_ERR_INVALID_ARG;
-  if (moe::row_kernel_grid(rows, d_ff) > kMaxGrid) return MOE_ERR_UNSUPPORTED;
+  if (moe::row_kernel_grid(rows, d_ff) > moe::kMaxWorkgroups) return MOE_ERR_UNSUPPORTED;
   return hip_status(moe::launch_swiglu_backward(dh, dtype == MOE_BF16, g, u, held, g_scales, u_scales, offsets,
                                                 E, rows, d_ff, dg, du, h, static_cast<hipStream_t>(stream)));
 }
@@ -572,7 +570,7 @@ moe_status_t moe_combine_backward(const void* dy, moe_dtype_t dy_dtype, const fl
   if (!ok_ptr(dy, (long long)T * d, 16) || !ok_ptr(topk_gates, R, 4) || !ok_ptr(dy_sorted, R * d, 16))
     return MOE_ERR_INVALID_ARG;
   if ((y_sorted || dgates) && (!ok_ptr(y_sorted, R * d, 16) || !ok_ptr(dgates, R, 4))) return MOE_ERR_INVALID_ARG;
-  if (moe::combine_backward_grid(T, k, d) > kMaxGrid) return MOE_ERR_UNSUPPORTED;
+  if (moe::combine_backward_grid(T, k, d) > moe::kMaxWorkgroups) return MOE_ERR_UNSUPPORTED;
   return hip_status(moe::launch_combine_backward(dy, dy_dtype == MOE_BF16, y_sorted, flat_to_sorted, topk_gates,
                                                  T, k, d, dy_sorted, dys_dtype == MOE_BF16, dgates,
                                                  static_cast<hipStream_t>(stream)));
@@ -586,7 +584,7 @@ moe_status_t moe_permute_backward(const void* dx_sorted, moe_dtype_t dtype,
   if (s == MOE_OK) s = check_float_dtype(dx_dtype);
   if (s != MOE_OK) return s;
   if (!ok_ptr(dx_sorted, (long long)T * k * d, 16) || !ok_ptr(dx, (long long)T * d, 16)) return MOE_ERR_INVALID_ARG;
-  if (moe::row_kernel_grid(T, d) > kMaxGrid) return MOE_ERR_UNSUPPORTED;
+  if (moe::row_kernel_grid(T, d) > moe::kMaxWorkgroups) return MOE_ERR_UNSUPPORTED;
   return hip_status(moe::launch_permute_backward(dx_sorted, dtype == MOE_BF16, flat_to_sorted, T, k, d, dx,
                                                  dx_dtype == MOE_BF16, static_cast<hipStream_t>(stream)));
 }
@@ -600,6 +598,7 @@ moe_status_t moe_route_backward(const float* dgates, const int32_t* topk_ids,
   if (!ok_ptr(dgates, R, 4) || !ok_ptr(topk_ids, R, 4) || !ok_ptr(topk_gates, R, 4) ||
       !ok_ptr(dlogits, (long long)T * E, 4))
     return MOE_ERR_INVALID_ARG;
+  if ((T + 3LL) / 4 > moe::kMaxWorkgroups) return MOE_ERR_UNSUPPORTED;
   return hip_status(moe::launch_route_backward(dgates, topk_ids, topk_gates, T, E, k, dlogits,
                                                static_cast<hipStream_t>(stream)));
 }

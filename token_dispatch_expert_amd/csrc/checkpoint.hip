@@ -144,7 +144,10 @@ __global__ __launch_bounds__(kRowThreads) void swiglu_backward_kernel(RowMap m, 
 
 }  // namespace
 
-long long row_kernel_grid(long long rows, int d) { return row_grid(row_map((d + 127) / 128 * 16), rows); }
+long long row_kernel_grid(long long rows, int d) {
+  const long long whole_groups = row_grid(row_map((d + 127) / 128 * 16), rows), plain = row_grid(row_map(d / 8), rows);
+  return whole_groups > plain ? whole_groups : plain;
+}
 
 hipError_t launch_pack(const void* x, bool bf16, int rows, int d, void* codes, float* scales, hipStream_t stream) {
   if (rows == 0) return hipSuccess;

@@ -656,7 +656,13 @@ hipError_t launch_product(const GroupedGemmArgs& a, int cus, hipStream_t stream)
 }  // namespace
 
 bool grouped_gemm_fits(const GroupedGemmArgs& a, GroupedProduct kind) {
-  return xcd_grid(tile_items(kind, a, 16, 64)) <= 0x7fffffffLL;  // the smallest tiles
+  // the smallest tiles that launch_product may take
+  const long long mean = a.rows / a.E;
+  int TM = 64, TN = 64;
+  if (kind == kWgrad) TM = TN = a.bf16 ? 128 : 64;
+  else if (a.bf16) TM = mean >= 12 ? 64 : 32, TN = mean >= 12 ? 128 : 64;
+  else if (mean < 48) TM = 16;
+  return xcd_grid(tile_items(kind, a, TM, TN)) <= kMaxWorkgroups;
 }
 
 hipError_t launch_grouped_gemm(const GroupedGemmArgs& a, GroupedProduct kind, hipStream_t stream) {

@@ -106,6 +106,9 @@ hipError_t launch_combine(const float* y_sorted, const int32_t* flat_to_sorted,
                           const float* gates, int T, int k, int d, void* y, bool bf16_out,
                           hipStream_t stream);
 
+// Most workgroups of a launch, at 256 threads: a launch's threads are counted in 32 bits.
+constexpr long long kMaxWorkgroups = 0xffffffffLL / 256;
+
 // Matrix products grouped by expert (grouped_gemm.hip). Operands in bf16 or fp32; W [E, N, K].
 //   forward  a = x [rows, K],  b = W,              out [rows, N]
 //   dgrad    a = dy [rows, N], b = W (a2, b2: a second pair or null), out [rows, K]
@@ -123,7 +126,7 @@ bool grouped_gemm_fits(const GroupedGemmArgs& a, GroupedProduct kind);
 hipError_t launch_grouped_gemm(const GroupedGemmArgs& a, GroupedProduct kind, hipStream_t stream);
 
 // Row-wise kernels of the training step (checkpoint.hip, backward.hip); d, f multiples of 8.
-long long row_kernel_grid(long long rows, int d);  // workgroups (to check against the grid limit)
+long long row_kernel_grid(long long rows, int d);  // workgroups, at most
 hipError_t launch_pack(const void* x, bool bf16, int rows, int d, void* codes, float* scales,
                        hipStream_t stream);
 // f2s [T, k] (the row of each of token t's assignments) or null: out row t
