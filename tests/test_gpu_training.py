@@ -426,3 +426,51 @@ def test_training_step_captured_and_replayed(dev, T, E, k, d, f, dtype):
             torch.cuda.synchronize()
             for n in names:
                 assert torch.equal(got[n], s.b[n]), (rep, i, n)
+
+
+def test_rows_past_32_bits(dev):
+    """Element offsets past 2^32 in every row-wise call, checked on the last rows."""
+    T, k, d = 75000, 8, 7168                                 # 4.3e9 elements in the sorted rows
+    R, m = T * k, 16
+    f2s = torch.arange(R, device=dev, dtype=torch.int32)     # token t's rows are t*k .. t*k + k - 1
+    gates = torch.full((T, k), 0.5, device=dev)
+    x = torch.zeros((T, d), dtype=BF, device=dev)
+    x[-2:] = normal((2, d), 1, dev)
+    ys = torch.zeros((R, d), device=dev)
+    ys[-m:] = normal((m, d), 2, dev)
+    rows, dgates = torch.full((R, d), float("nan"), dtype=BF, device=dev), torch.empty((T, k), device=dev)
+    moe.moe_combine_backward(x, ys, f2s, gates, rows, dgates)
+    last = x[-2:].repeat_interleave(k, 0)
+    assert torch.equal(rows[-m:], (last.float() * 0.5).to(BF)) and (rows[:m] == 0).all()
+    want = (last.double() * ys[-m:].double()).sum(1)
+    assert (dgates[-2:].reshape(-1).double() - want).abs().max() <= d * 2.0 ** -23 * (last.double() * ys[-m:].double()).abs().sum(1).max()
+    del ys
+    codes, scales = torch.empty((T, d), dtype=F8, device=dev), torch.empty((T, d // 128), device=dev)
+    moe.moe_checkpoint_pack(x, codes, scales)
+    rows.fill_(float("nan"))
+    moe.moe_checkpoint_unpack(codes, scales, rows, flat_to_sorted=f2s)
+    assert torch.equal(rows[-m:], ref.held(x[-2:])[0].to(BF).to(dev).repeat_interleave(k, 0)) and not torch.isnan(rows).any()
+    dx = torch.empty((T, d), device=dev)
+    moe.moe_permute_backward(rows, f2s, k, dx)
+    assert torch.equal(dx[-2:].double(), rows[-m:].double().reshape(2, k, d).sum(1)) and (dx[0] == 0).all()
+    # 4.4e9 elements of the activations
+    g = rows
+    g.zero_()
+    g[-m:] = normal((m, d), 3, dev)
+    u_, h = g.clone(), torch.full_like(g, float("nan"))
+    c = [torch.empty((R, d), dtype=F8, device=dev) for _ in range(2)]
+    s = [torch.empty((R, d // 128), device=dev) for _ in range(2)]
+    moe.moe_swiglu(g, u_, h, c[0], s[0], c[1], s[1])
+    gd = g[-m:].double()
+    tol = swiglu_tolerances(gd, gd, gd, BF)
+    assert ((h[-m:].double() - ref.swiglu(gd, gd)).abs() <= tol["h"]).all() and (h[:m] == 0).all()
+    hold = ref.held(g[-m:])[0].to(dev)
+    dg, du = u_, g  # (their values are held in 8 bits now)
+    dh = h.fill_(0.0)
+    dh[-m:] = 1.0
+    moe.moe_swiglu_backward(dh, c[0], c[1], dg, du, g_scales=s[0], u_scales=s[1])
+    one = torch.ones_like(hold)
+    want = dict(zip(("dg", "du", "h"), ref.swiglu_backward(one, hold, hold)))
+    tol = swiglu_tolerances(hold, hold, one, BF)
+    assert ((dg[-m:].double() - want["dg"]).abs() <= tol["dg"]).all()
+    assert ((du[-m:].double() - want["du"]).abs() <= tol["du"]).all()
