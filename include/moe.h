@@ -35,12 +35,14 @@
  *    are then unspecified.
  *  - Sizes: T tokens, E experts, k experts per token, d hidden size, d_ff expert width,
  *    R = T*k routed rows. Limits: 0 <= T, 1 <= E <= MOE_MAX_EXPERTS, 1 <= k <= min(E,
- *    MOE_MAX_TOPK), T*k*max(d, d_ff) < 2^31. T = 0 is a valid empty call.
+ *    MOE_MAX_TOPK), T*k*max(d, d_ff) < 2^31 (not in the training calls, which state their own).
+ *    T = 0 is a valid empty call.
  *  - Alignment: every pointer 16-byte aligned.
  *  - Determinism: no floating-point atomics; repeated calls give bit-identical results.
  *
  * Number formats (moe_dtype_t): fp32, bf16, and OCP fp8 e4m3fn (1 sign, 4 exponent bits with
- * bias 7, 3 mantissa bits, no infinities, max 448) for weights only; and, for weights only,
+ * bias 7, 3 mantissa bits, no infinities, max 448) for weights and for rows held between a
+ * forward and a backward pass (moe_checkpoint_pack); and, for weights only,
  * MOE_BF16_BLOCKED and MOE_FP8_E4M3FN_BLOCKED: bf16 / fp8 e4m3fn values with each [N, K] matrix
  * (K its contraction axis) stored in blocks of 8 rows x 128 bytes (64 bf16 or 128 fp8
  * contraction elements), each block 1 KB contiguous: [N/8][K/64][8][64] for bf16,

@@ -417,7 +417,8 @@ def moe_grouped_gemm(x, offsets, w, y, stream=None):
     _need(w, x.dtype, (E, N, K), "w")
     _need(offsets, torch.int32, (E + 1,), "offsets")
     _need(y, y.dtype, (rows, N), "y")
-    _call("moe_grouped_gemm", stream, x, _float_dt(x, "x"), offsets, rows, E, N, K, w, _float_dt(w, "w"), y, _float_dt(y, "y"))
+    _call("moe_grouped_gemm", stream, x, _float_dt(x, "x"), offsets, rows, E, N, K, w,
+          _float_dt(w, "w"), y, _float_dt(y, "y"))
 
 
 def moe_grouped_gemm_dgrad(dy, offsets, w, dx, dy2=None, w2=None, stream=None):
@@ -433,8 +434,8 @@ def moe_grouped_gemm_dgrad(dy, offsets, w, dx, dy2=None, w2=None, stream=None):
     if dy2 is not None:
         _need(dy2, dy.dtype, (rows, N), "dy2")
         _need(w2, dy.dtype, (E, N, K), "w2")
-    _call("moe_grouped_gemm_dgrad", stream, dy, dy2, _float_dt(dy, "dy"), offsets, rows, E, N, K, w, w2, _float_dt(w, "w"), dx,
-          _float_dt(dx, "dx"))
+    _call("moe_grouped_gemm_dgrad", stream, dy, dy2, _float_dt(dy, "dy"), offsets, rows, E, N, K, w,
+          w2, _float_dt(w, "w"), dx, _float_dt(dx, "dx"))
 
 
 def moe_grouped_gemm_wgrad(dy, x, offsets, dw, accumulate: bool = False, stream=None):
@@ -446,7 +447,8 @@ def moe_grouped_gemm_wgrad(dy, x, offsets, dw, accumulate: bool = False, stream=
     _need(x, dy.dtype, (rows, K), "x")
     _need(offsets, torch.int32, (E + 1,), "offsets")
     _need(dw, dw.dtype, (E, N, K), "dw")
-    _call("moe_grouped_gemm_wgrad", stream, dy, x, _float_dt(dy, "dy"), offsets, rows, E, N, K, dw, _float_dt(dw, "dw"), int(bool(accumulate)))
+    _call("moe_grouped_gemm_wgrad", stream, dy, x, _float_dt(dy, "dy"), offsets, rows, E, N, K, dw,
+          _float_dt(dw, "dw"), int(bool(accumulate)))
 
 
 def moe_checkpoint_pack(x, codes, scales, stream=None):
@@ -468,7 +470,8 @@ def moe_checkpoint_unpack(codes, scales, out, flat_to_sorted=None, stream=None):
     if T and rows % T:
         raise ValueError("flat_to_sorted must have k entries for every row")
     _need(out, out.dtype, (rows, d), "out")
-    _call("moe_checkpoint_unpack", stream, codes, scales, T, rows // T if T else 1, d, flat_to_sorted, out, _float_dt(out, "out"))
+    _call("moe_checkpoint_unpack", stream, codes, scales, T, rows // T if T else 1, d,
+          flat_to_sorted, out, _float_dt(out, "out"))
 
 
 def moe_swiglu(g, u, h, g_codes=None, g_scales=None, u_codes=None, u_scales=None, offsets=None, stream=None):
@@ -513,7 +516,8 @@ def moe_swiglu_backward(dh, g, u, dg, du, h=None, g_scales=None, u_scales=None, 
         _held(u, u_scales, (rows, f), "u")
         gu = MOE_FP8_E4M3FN
     E = _row_offsets(offsets)
-    _call("moe_swiglu_backward", stream, dh, _float_dt(dh, "dh"), g, u, gu, g_scales, u_scales, offsets, E, rows, f, dg, du, h)
+    _call("moe_swiglu_backward", stream, dh, _float_dt(dh, "dh"), g, u, gu, g_scales, u_scales,
+          offsets, E, rows, f, dg, du, h)
 
 
 def moe_combine_backward(dy, y_sorted, flat_to_sorted, topk_gates, dy_sorted, dgates, stream=None):
@@ -529,8 +533,8 @@ def moe_combine_backward(dy, y_sorted, flat_to_sorted, topk_gates, dy_sorted, dg
     if dgates is not None:
         _need(y_sorted, torch.float32, (T * k, d), "y_sorted")
         _need(dgates, torch.float32, (T, k), "dgates")
-    _call("moe_combine_backward", stream, dy, _float_dt(dy, "dy"), y_sorted, flat_to_sorted, topk_gates, T, k, d, dy_sorted,
-          _float_dt(dy_sorted, "dy_sorted"), dgates)
+    _call("moe_combine_backward", stream, dy, _float_dt(dy, "dy"), y_sorted, flat_to_sorted,
+          topk_gates, T, k, d, dy_sorted, _float_dt(dy_sorted, "dy_sorted"), dgates)
 
 
 def moe_permute_backward(dx_sorted, flat_to_sorted, k: int, dx, stream=None):
@@ -538,7 +542,8 @@ def moe_permute_backward(dx_sorted, flat_to_sorted, k: int, dx, stream=None):
     T, d = _dims(dx, 2, "dx")
     _need(dx_sorted, dx_sorted.dtype, (T * k, d), "dx_sorted")
     _need(flat_to_sorted, torch.int32, (T * k,), "flat_to_sorted")
-    _call("moe_permute_backward", stream, dx_sorted, _float_dt(dx_sorted, "dx_sorted"), flat_to_sorted, T, k, d, dx, _float_dt(dx, "dx"))
+    _call("moe_permute_backward", stream, dx_sorted, _float_dt(dx_sorted, "dx_sorted"),
+          flat_to_sorted, T, k, d, dx, _float_dt(dx, "dx"))
 
 
 def moe_route_backward(dgates, topk_ids, topk_gates, dlogits, stream=None):

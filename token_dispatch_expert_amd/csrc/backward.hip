@@ -6,6 +6,10 @@
 //   route    gate = softmax of the k chosen logits dlogit[t, id_j] = g_j (dg_j - sum_i g_i dg_i)
 // p(t, j) = flat_to_sorted[t*k + j]; an entry that names no row (an assignment dropped for its
 // expert's capacity) has no gradient. Sums are fp32 in a fixed order, without atomics.
+//
+// All three are bound by HBM. 8,192 tokens, 8 experts each, d = 7168, bf16 gradients: combine 540 - 570
+// us (2.9 GB: y_sorted once, dy once per token, dy_sorted written; 5.2 - 5.4 TB/s, where a copy of
+// 2 GiB reaches 4.8), permute 168 us (1.06 GB, 6.3 TB/s), route 8 us for 256 experts.
 #include "rows.h"
 
 namespace moe {
@@ -20,7 +24,8 @@ __device__ __forceinline__ int sorted_row(const int32_t* f2s, long long i, int R
 
 // One assignment (t, j) per group of WAVES waves: 4 / WAVES assignments per workgroup. A
 // token's k assignments go to consecutive workgroups of one XCD (workgroup b runs on XCD
-// b % 8), so that dy[t] is read from HBM once and then from that XCD's L2.
+// b % 8), so that dy[t] is read from HBM once and then from that XCD's L2. One workgroup for all of a
+// token's assignments, with dy[t] in registers, took 571 us against 541.
 template <typename TI, typename TO, int WAVES>
 __global__ __launch_bounds__(256) void combine_backward_kernel(const TI* __restrict__ dy,
                                                               const float* __restrict__ ys,

@@ -440,6 +440,22 @@ __device__ __forceinline__ void bare_barrier() {
 // DEAL: each wave runs a loop compiled for the number of its 16-row fragments that hold rows, so
 // a partial tile costs what its rows need; waves w and w + 4 share a SIMD and own different
 // halves of the tile, so every SIMD has work.
+//
+// Measured, 65,536 rows dealt by Zipf 1.2 to 32 experts of 2048 x 7168 (bf16): forward 1.60 ms
+// (1.20 PFLOP/s), two input gradients 3.11 ms (1.24), fp32 weight gradients 1.85 ms (1.04); a
+// library product of these sizes without the experts reaches 1.34, 1.13 and 1.02. The clock
+// falls to 1.9 - 2.05 GHz under the power limit; of the cycles the matrix instructions take 59%
+// (forward, input gradients) and 47% (weight gradients, whose 1.9 GB of fp32 stores take another
+// 20%). LDS is busy 18 - 23% without bank conflicts; taking out, one by one, LDS reads, loads that
+// hit in the L2 and those that miss it gives back about 9% of the time each. Few rows are bound by the
+// stream of the weights: 1,024 rows over 128 experts of 1536 x 4096 take 245 us (1.6 GB, 6.5 TB/s),
+// 8 rows on 8 of them 18 us (101 MB, 5.6 TB/s).
+//
+// The tile: 256 x 256 with 8 waves of 128 x 64 has the most products per byte that the registers
+// of 8 waves hold, and its two slots of 64 fill 128 KB of LDS. Slower were 4 or 5 slots of 32 (1.83 ms
+// forward), a slot more for one operand (1.72), two workgroups per CU with half the tile (2.41),
+// 4 waves of 128 x 128 (accumulators move between register files), and workgroups that stay and load
+// the next tile's first steps under the last products (1.66).
 template <GroupedProduct P, int WM, int WN, int WGM, int WGN, int DK, int RING, bool ONCE, bool DEAL>
 __global__ __launch_bounds__(64 * WGM * WGN) void tile_kernel(ProductArgs p) {
   constexpr bool AX = P == kWgrad, BX = P != kForward;
