@@ -7,9 +7,9 @@
 // p(t, j) = flat_to_sorted[t*k + j]; an entry that names no row (an assignment dropped for its
 // expert's capacity) has no gradient. Sums are fp32 in a fixed order, without atomics.
 //
-// All three are bound by HBM. 8,192 tokens, 8 experts each, d = 7168, bf16 gradients: combine 540 - 570
-// us (2.9 GB: y_sorted once, dy once per token, dy_sorted written; 5.2 - 5.4 TB/s, where a copy of
-// 2 GiB reaches 4.8), permute 168 us (1.06 GB, 6.3 TB/s), route 8 us for 256 experts.
+// All three are bound by HBM. 8,192 tokens, 8 experts each, d = 7168, bf16 gradients: combine 540 us
+// (2.9 GB: y_sorted once, dy once per token, dy_sorted written; 5.4 TB/s, where a copy of 2 GiB
+// reaches 4.8), permute 168 us (1.06 GB, 6.3 TB/s), route 8 us for 256 experts.
 #include "rows.h"
 
 namespace moe {
@@ -26,7 +26,8 @@ __device__ __forceinline__ int sorted_row(const int32_t* f2s, long long i, int R
 // token's k assignments go to consecutive workgroups of one XCD (workgroup b runs on XCD
 // b % 8), so that dy[t] is read from HBM once and then from that XCD's L2. One workgroup for all of a
 // token's assignments, with dy[t] in registers, took 571 us against 541.
-template <typename TI, typename TO, int WAVES>
+// STREAM: dys is stored non-temporally (a branch in the kernel would be merged into plain stores).
+template <typename TI, typename TO, int WAVES, bool STREAM>
 __global__ __launch_bounds__(256) void combine_backward_kernel(const TI* __restrict__ dy,
                                                               const float* __restrict__ ys,
                                                               const int32_t* __restrict__ f2s,
@@ -53,7 +54,8 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(const TI* __restr
       F8 o;
 #pragma unroll
       for (int q = 0; q < 8; ++q) o.v[q] = g * v.v[q];
-      store8(dst + c, o);  // (non-temporal: 540 against 545 us at 65,536 rows, but 21 against 17 at 4,096)
+      if constexpr (STREAM) store8_once(dst + c, o);
+      else store8(dst + c, o);
       if (y) {
         const F8 w = load8_once(y + c);
 #pragma unroll
@@ -131,6 +133,9 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const float* __rest
 // Workgroups of combine_backward_kernel: a row takes a whole workgroup from 1024 elements on
 // (two units of 8 per thread and less leave waves idle below), else a wave.
 constexpr int kWideRow = 1024;
+// Rows written that do not fit the 256 MB last-level cache are stored non-temporally: 940 MB of them
+// 540 us against 570; 235 MB, which the next product finds there, 138 against 133.
+constexpr long long kCacheBytes = 256LL << 20;
 
 template <typename TI, typename TO>
 hipError_t launch_combine_backward_t(const void* dy, const float* ys, const int32_t* f2s, const float* gates,
@@ -138,7 +143,9 @@ hipError_t launch_combine_backward_t(const void* dy, const float* ys, const int3
   const unsigned grid = (unsigned)combine_backward_grid(T, k, d);
   const TI* s = static_cast<const TI*>(dy);
   TO* o = static_cast<TO*>(dys);
-  auto kern = d > kWideRow ? &combine_backward_kernel<TI, TO, 4> : &combine_backward_kernel<TI, TO, 1>;
+  const bool past_cache = (long long)T * k * d * (long long)sizeof(TO) > kCacheBytes;
+  auto kern = d > kWideRow ? (past_cache ? &combine_backward_kernel<TI, TO, 4, true> : &combine_backward_kernel<TI, TO, 4, false>)
+                           : (past_cache ? &combine_backward_kernel<TI, TO, 1, true> : &combine_backward_kernel<TI, TO, 1, false>);
   kern<<<grid, 256, 0, stream>>>(s, ys, f2s, gates, T, k, d, o, dgates);
   return hipGetLastError();
 }
