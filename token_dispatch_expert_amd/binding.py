@@ -121,9 +121,9 @@ def _stream(stream):
 
 
 def _need(t, dtype, shape, name):
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.shape != tuple(shape):
+    if t.shape != shape and t.shape != tuple(shape):
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
@@ -357,13 +357,19 @@ def moe_layer(logits, x, w_gate, w_up, w_down, k: int, out: dict, workspace: Wor
 # ----------------------------------------------------------------------------------------
 # training: the pieces of the layer's gradient (same names as the C ABI)
 # ----------------------------------------------------------------------------------------
+_Tensor = torch.Tensor
+_FLOAT_DT = {t: _DTYPE_ENUM[t] for t in (torch.float32, torch.bfloat16)}
+_CODE_DT = (torch.float8_e4m3fn, torch.uint8)
+
+
+# A small call is bound by the host, so these checks look each property of a tensor up once.
 def _call(name: str, stream, *args):
     """Enqueue lib.<name>(*args, stream), tensors among args as their addresses, on the device that
     every tensor is on, whichever is current: on `stream`, or on that device's current stream."""
     device = None
     raw = []
     for a in args:
-        if isinstance(a, torch.Tensor):
+        if isinstance(a, _Tensor):
             d = a.get_device()
             if d != device:
                 if d < 0:
@@ -380,7 +386,7 @@ def _call(name: str, stream, *args):
     fn = getattr(_lib if _lib is not None else load_library(), name)
     # (the raw handle of the current stream: 0.2 us, against 2.7 for torch.cuda.current_stream())
     handle = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
-    if device == torch.cuda.current_device():
+    if device == torch._C._cuda_getDevice():  # (torch.cuda.current_device() without its set-up check)
         status = fn(*raw, handle)
     else:
         with torch.cuda.device(device):
@@ -390,23 +396,26 @@ def _call(name: str, stream, *args):
 
 
 def _float_dt(t, name):
-    if t.dtype not in (torch.float32, torch.bfloat16):
+    dt = _FLOAT_DT.get(t.dtype)
+    if dt is None:
         raise TypeError(f"{name}: expected float32 or bfloat16, got {t.dtype}")
-    return _DTYPE_ENUM[t.dtype]
+    return dt
 
 
 def _dims(t, n, name):
-    if t.dim() != n:
-        raise ValueError(f"{name}: expected {n} dimensions, got shape {tuple(t.shape)}")
-    return t.shape
+    shape = t.shape
+    if len(shape) != n:
+        raise ValueError(f"{name}: expected {n} dimensions, got shape {tuple(shape)}")
+    return shape
 
 
 def _held(codes, scales, shape, name):
     """codes (float8_e4m3fn or uint8) and scales of rows held in 8 bits."""
-    if codes.dtype not in (torch.float8_e4m3fn, torch.uint8):
-        raise TypeError(f"{name}_codes: expected float8_e4m3fn or uint8, got {codes.dtype}")
-    _need(codes, codes.dtype, shape, f"{name}_codes")
-    _need(scales, torch.float32, (shape[0], -(-shape[1] // 128)), f"{name}_scales")
+    dt = codes.dtype
+    if dt not in _CODE_DT:
+        raise TypeError(f"{name}_codes: expected float8_e4m3fn or uint8, got {dt}")
+    _need(codes, dt, shape, name + "_codes")
+    _need(scales, torch.float32, (shape[0], -(-shape[1] // 128)), name + "_scales")
 
 
 def moe_grouped_gemm(x, offsets, w, y, stream=None):
@@ -477,47 +486,49 @@ def moe_checkpoint_unpack(codes, scales, out, flat_to_sorted=None, stream=None):
 def moe_swiglu(g, u, h, g_codes=None, g_scales=None, u_codes=None, u_scales=None, offsets=None, stream=None):
     """h = silu(g) * u, all [rows, d_ff] in one dtype (bfloat16 or float32); with codes and scales, g
     and u are held in 8 bits too. offsets [E+1]: only rows below offsets[E]."""
-    rows, f = _dims(g, 2, "g")
-    _need(u, g.dtype, (rows, f), "u")
-    _need(h, g.dtype, (rows, f), "h")
-    held = (g_codes, g_scales, u_codes, u_scales)
-    if any(t is not None for t in held):
-        if any(t is None for t in held):
+    shape = _dims(g, 2, "g")
+    _need(u, g.dtype, shape, "u")
+    _need(h, g.dtype, shape, "h")
+    if not (g_codes is None and g_scales is None and u_codes is None and u_scales is None):
+        if g_codes is None or g_scales is None or u_codes is None or u_scales is None:
             raise ValueError("g_codes, g_scales, u_codes and u_scales come together")
-        _held(g_codes, g_scales, (rows, f), "g")
-        _held(u_codes, u_scales, (rows, f), "u")
+        _held(g_codes, g_scales, shape, "g")
+        _held(u_codes, u_scales, shape, "u")
     E = _row_offsets(offsets)
-    _call("moe_swiglu", stream, g, u, _float_dt(g, "g"), offsets, E, rows, f, h, *held)
+    _call("moe_swiglu", stream, g, u, _float_dt(g, "g"), offsets, E, *shape, h, g_codes, g_scales,
+          u_codes, u_scales)
 
 
 def _row_offsets(offsets) -> int:
     if offsets is None:
         return 0
-    E = offsets.numel() - 1
-    _need(offsets, torch.int32, (E + 1,), "offsets")
-    return E
+    E, = _dims(offsets, 1, "offsets")
+    _need(offsets, torch.int32, (E,), "offsets")
+    return E - 1
 
 
 def moe_swiglu_backward(dh, g, u, dg, du, h=None, g_scales=None, u_scales=None, offsets=None, stream=None):
     """dg and du (and h again, if given) from dh, all [rows, d_ff] in dh's dtype; g and u in that dtype,
     or held in 8 bits (codes, with g_scales and u_scales)."""
-    rows, f = _dims(dh, 2, "dh")
-    for t, n in ((dg, "dg"), (du, "du"), (h, "h")):
-        if t is not None:
-            _need(t, dh.dtype, (rows, f), n)
+    shape = _dims(dh, 2, "dh")
+    dt = dh.dtype
+    _need(dg, dt, shape, "dg")
+    _need(du, dt, shape, "du")
+    if h is not None:
+        _need(h, dt, shape, "h")
     if g_scales is None and u_scales is None:
-        _need(g, dh.dtype, (rows, f), "g")
-        _need(u, dh.dtype, (rows, f), "u")
+        _need(g, dt, shape, "g")
+        _need(u, dt, shape, "u")
         gu = _float_dt(g, "g")
     elif g_scales is None or u_scales is None:
         raise ValueError("g_scales and u_scales come together")
     else:
-        _held(g, g_scales, (rows, f), "g")
-        _held(u, u_scales, (rows, f), "u")
+        _held(g, g_scales, shape, "g")
+        _held(u, u_scales, shape, "u")
         gu = MOE_FP8_E4M3FN
     E = _row_offsets(offsets)
     _call("moe_swiglu_backward", stream, dh, _float_dt(dh, "dh"), g, u, gu, g_scales, u_scales,
-          offsets, E, rows, f, dg, du, h)
+          offsets, E, *shape, dg, du, h)
 
 
 def moe_combine_backward(dy, y_sorted, flat_to_sorted, topk_gates, dy_sorted, dgates, stream=None):
