@@ -133,9 +133,6 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const float* __rest
 // Workgroups of combine_backward_kernel: a row takes a whole workgroup from 1024 elements on
 // (two units of 8 per thread and less leave waves idle below), else a wave.
 constexpr int kWideRow = 1024;
-// Rows written that do not fit the 256 MB last-level cache are stored non-temporally: 940 MB of them
-// 540 us against 570; 235 MB, which the next product finds there, 138 against 133.
-constexpr long long kCacheBytes = 256LL << 20;
 
 template <typename TI, typename TO>
 hipError_t launch_combine_backward_t(const void* dy, const float* ys, const int32_t* f2s, const float* gates,
@@ -143,6 +140,8 @@ hipError_t launch_combine_backward_t(const void* dy, const float* ys, const int3
   const unsigned grid = (unsigned)combine_backward_grid(T, k, d);
   const TI* s = static_cast<const TI*>(dy);
   TO* o = static_cast<TO*>(dys);
+  // Rows that do not fit the last-level cache are stored non-temporally: 940 MB of them 540 us against
+  // 570; 235 MB, which the next product finds there, 138 against 133.
   const bool past_cache = (long long)T * k * d * (long long)sizeof(TO) > kCacheBytes;
   auto kern = d > kWideRow ? (past_cache ? &combine_backward_kernel<TI, TO, 4, true> : &combine_backward_kernel<TI, TO, 4, false>)
                            : (past_cache ? &combine_backward_kernel<TI, TO, 1, true> : &combine_backward_kernel<TI, TO, 1, false>);

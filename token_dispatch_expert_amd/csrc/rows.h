@@ -6,6 +6,7 @@
 namespace moe {
 
 constexpr int kRowThreads = 256;
+constexpr long long kCacheBytes = 256LL << 20;  // the last-level cache
 
 // Workgroups over rows of `units` 8-element units: 2^shift threads and `slices` workgroups per
 // row. Rows of at least 64 units have workgroups of their own (of 2^shift threads, so the row and
@@ -53,8 +54,8 @@ struct F8 {
   float v[8];
 };
 // ..._once: non-temporal, for data that the kernel reads or writes once: its lines leave the caches
-// first. At 65,536 rows the SwiGLU gradient took 235 us without and 214 us with them, unpacking
-// 194 and 181; loads of rows that several workgroups read stay plain.
+// first. At 65,536 rows of 2048 the SwiGLU gradient took 235 us without and 214 us with them; loads of rows
+// that several workgroups read stay plain, and stores where a kernel says why.
 __device__ __forceinline__ F8 load8_once(const float* p) {
   const f32x4 a = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p));
   const f32x4 b = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p + 4));
