@@ -44,6 +44,7 @@ struct ProductArgs {
   const int32_t* offsets;
   int rows, E, N, K;
   int out_bf16, accumulate;
+  int stream;  // C's rows are stored non-temporally
 };
 
 // The value of the lane 8 further within the 16.
@@ -84,14 +85,18 @@ struct OutTile {
                                            mlim * ld - c0 * size, kBufferWord3);
   }
   __device__ __forceinline__ int at(int r, int c, int size) const { return c < clim ? r * ld + c * size : kOutside; }
+  __device__ __forceinline__ void put(u32x4 x, int at, bool stream) const {
+    if (stream) __builtin_amdgcn_raw_buffer_store_b128(x, to, at, 0, kNonTemporal);
+    else __builtin_amdgcn_raw_buffer_store_b128(x, to, at, 0, 0);
+  }
 };
 
 // 16 rows of C from r0 and NF * 16 columns from c0 of the tile. `v` is as the products leave it: 4
 // consecutive columns (from 4 (lane / 16)) of row lane % 16 in each 16-column fragment. Stored
 // like that, an instruction would write 64 bytes (fp32) or 32 (bf16) of each of 16 rows; lanes
 // first exchange parts so that it writes 128 bytes of each of 8 (2% of the large products' time),
-// non-temporal, which leaves the L2 to the operands (weight gradients of 128 rows per expert: 526
-// against 424 us).
+// most often non-temporally (stream_rows), which leaves the L2 to the operands (weight gradients of
+// 128 rows per expert: 526 against 424 us).
 template <int NF>
 __device__ __forceinline__ void store_fragments(const OutTile& o, const ProductArgs& p, const f32x4 (&v)[NF], int r0,
                                                 int c0, int lane) {
@@ -101,8 +106,7 @@ __device__ __forceinline__ void store_fragments(const OutTile& o, const ProductA
       for (int j = 0; j < NF; j += 2)
         store_row_halves(__builtin_bit_cast(u32x4, v[j]), __builtin_bit_cast(u32x4, v[j + 1]), lane,
                          [&](int r, int part, u32x4 x) __attribute__((always_inline)) {
-                           const int c = c0 + (j + part) * 16 + (lane >> 4) * 4;
-                           __builtin_amdgcn_raw_buffer_store_b128(x, o.to, o.at(r0 + r, c, 4), 0, kNonTemporal);
+                           o.put(x, o.at(r0 + r, c0 + (j + part) * 16 + (lane >> 4) * 4, 4), p.stream);
                          });
       return;
     }
@@ -123,8 +127,7 @@ __device__ __forceinline__ void store_fragments(const OutTile& o, const ProductA
       for (int j = 0; j < NF / 2; j += 2)
         store_row_halves(q[j], q[j + 1], lane, [&](int r, int part, u32x4 x) __attribute__((always_inline)) {
           const int g = lane >> 4;
-          const int c = c0 + (j + part) * 32 + (g & 1) * 16 + (g >> 1) * 8;
-          __builtin_amdgcn_raw_buffer_store_b128(x, o.to, o.at(r0 + r, c, 2), 0, kNonTemporal);
+          o.put(x, o.at(r0 + r, c0 + (j + part) * 32 + (g & 1) * 16 + (g >> 1) * 8, 2), p.stream);
         });
       return;
     }
@@ -432,6 +435,13 @@ __device__ __forceinline__ void bare_barrier() {
   __atomic_signal_fence(__ATOMIC_SEQ_CST);
 }
 
+// Until at most min(n, MOST) steps of LOADS loads each are in flight; n is the same in every lane.
+template <int LOADS, int MOST>
+__device__ __forceinline__ void wait_steps(int n) {
+  if (n >= MOST) wait_vmcnt<MOST * LOADS>();
+  else static_for<MOST>([&](auto i) { if (n == decltype(i)::value) wait_vmcnt<decltype(i)::value * LOADS>(); });
+}
+
 // A workgroup of WGM x WGN waves computes a tile of C, each wave WM x WN of it with
 // v_mfma_f32_16x16x32_bf16; steps of DK go through a ring of RING slots in LDS. While a
 // slice's products run, the fragments of the next slice are read (B into the other of two
@@ -489,7 +499,9 @@ __global__ __launch_bounds__(64 * WGM * WGN) void tile_kernel(ProductArgs p) {
   const ptrdiff_t moved_a = pair ? static_cast<const char*>(p.a2) - static_cast<const char*>(p.a) : 0;
   const ptrdiff_t moved_b = pair ? static_cast<const char*>(p.b2) - static_cast<const char*>(p.b) : 0;
   const int steps1 = (t.kdim + DK - 1) / DK, steps = pair ? 2 * steps1 : steps1;
-  const bool once = ONCE && t.rb - t.ra <= TM;  // the expert's weights are read by this row tile alone
+  // The expert's weights are read by this row tile alone, in whole lines (1,024 rows on 128 experts of
+  // 1536 x K, two input gradients: K = 4096 436 us against 476 with plain loads, K = 4104 509 against 457).
+  const bool once = ONCE && t.rb - t.ra <= TM && p.K % 64 == 0;
 
   auto issue = [&](int st) __attribute__((always_inline)) {
     u32x4* slot = ring + st % RING * STAGE;
@@ -517,7 +529,7 @@ __global__ __launch_bounds__(64 * WGM * WGN) void tile_kernel(ProductArgs p) {
 #pragma unroll
       for (int r = 0; r < RING; ++r)
         if (r < steps) issue(r);
-      wait_vmcnt_dyn<(RING - 1) * LOADS>(min(RING - 1, steps - 1) * LOADS);
+      wait_steps<LOADS, RING - 1>(steps - 1);
       bare_barrier();
 #pragma unroll
       for (int j = 0; j < (F ? NF : 0); ++j) fb[0][j] = OB::read(ring + OA::kChunks, wn + j * 16, 0, lane);
@@ -534,7 +546,7 @@ __global__ __launch_bounds__(64 * WGM * WGN) void tile_kernel(ProductArgs p) {
           if (st + 1 < steps) {
             // step st + 1 has landed for this wave, and after the barrier for all; all are done
             // with step st's slot
-            wait_vmcnt_dyn<(RING - 2) * LOADS>(min(RING - 2, steps - 2 - st) * LOADS);
+            wait_steps<LOADS, RING - 2>(steps - 2 - st);
             bare_barrier();
             if (st + RING < steps) issue(st + RING);
           }
@@ -619,10 +631,30 @@ double step_time(GroupedProduct kind, const GroupedGemmArgs& a, const TileCost& 
   return whole * c.full + (left == 0 ? 0 : left <= cus ? c.alone : c.full);
 }
 
+// Whether C's rows are stored non-temporally. Rows of whole 128-byte lines always are. Others share lines
+// between tiles and between a row's pieces; those lines are put together in the L2 if they may stay
+// there, which pays unless the products are long enough that the L2 is worth more to the operands
+// (16,384 rows over 8 experts of 3288 x K, bf16, plain and non-temporal: K = 264 60 and 70 us, 1032 130
+// and 141, 4104 507 and 495; weight gradients of 42 experts of 2488 x 3288, bf16: 64 rows per expert 220 and
+// 287 us, 256 376 and 334; fp32: 256 rows 496 and 612, 512 690 and 670).
+int stream_rows(const GroupedGemmArgs& a, GroupedProduct kind) {
+  const long long cols = kind == kForward ? a.N : a.K;
+  if (cols * (a.out_bf16 ? 2 : 4) % 128 == 0) return 1;
+  if (kind == kWgrad) return a.rows / a.E >= (a.out_bf16 ? 192 : 512);
+  return (kind == kForward ? a.K : a.N) >= 4096;
+}
+
+// Tiles of 32 rows that leave a CU to each (of one expert: exactly; of several: tile_items counts one
+// that may be partial for each).
+bool few_tiles(GroupedProduct kind, const GroupedGemmArgs& a, int TN, int cus) {
+  if (a.E > 1) return 2 * tile_items(kind, a, 32, TN) <= 3LL * cus;
+  return (a.rows + 31LL) / 32 * (((kind == kForward ? a.N : a.K) + TN - 1LL) / TN) <= cus;
+}
+
 template <GroupedProduct P>
 hipError_t launch_product(const GroupedGemmArgs& a, int cus, hipStream_t stream) {
   const ProductArgs p{a.a, a.b, a.a2, a.b2, a.out, a.offsets, a.rows, a.E, a.N, a.K,
-                      a.out_bf16 ? 1 : 0, a.accumulate ? 1 : 0};
+                      a.out_bf16 ? 1 : 0, a.accumulate ? 1 : 0, stream_rows(a, P)};
   if (!a.bf16) {
     // Few rows leave most of a 64-row tile's products empty: at 64 experts of 1024 x 2048, even rows,
     // tiles of 16 x 64 against 64 x 64 took (forward) 124 and 166 us at 1 row per expert, 128 and
@@ -657,6 +689,14 @@ hipError_t launch_product(const GroupedGemmArgs& a, int cus, hipStream_t stream)
       return launch_tiles<P, 128, 64, 2, 4, 64, 2, false, true>(a, p, stream);
     return launch_tiles<P, 64, 64, 2, 2, 64, 2, false, false>(a, p, stream);
   } else {
+    // With a CU to each tile, small tiles and as many steps in flight as the LDS holds: one expert of
+    // 1024 x 2048, forward, 256 rows 10.4 us against 18.7 in tiles of 64 x 128, 512 rows 11.7 against 18.5,
+    // 768 rows (384 tiles) 19.4 against 18.7; one token for 8 of 128 experts of 1536 x 4096 17.9 against
+    // 18.5 in the three-slot rings; the input gradient of two with 2048 x 1024, 256 rows 32.9 against 41.7.
+    if (few_tiles(P, a, P == kForward ? 64 : 128, cus)) {
+      if constexpr (P == kForward) return launch_tiles<P, 32, 16, 1, 4, 128, 6, true, false>(a, p, stream);
+      return launch_tiles<P, 32, 32, 1, 4, 64, 7, true, false>(a, p, stream);
+    }
     if (mean >= 96) {
       const double small = step_time(P, a, kSmall, cus);
       if (mean >= (P == kForward ? 192 : 96) && (P == kForward ? a.N : a.K) > 128 && big <= mid && big <= small)
