@@ -268,6 +268,15 @@ def test_every_tile_size_exact(dev, counts, N, K, out):
     run_all(counts, 3, N, K, BF, out, dev, seed=12)
 
 
+# Few tiles, each with a CU of its own and more steps than the ring has slots, or fewer, or a part of one
+@pytest.mark.parametrize("counts,N,K", [
+    ([40, 0, 3], 1544, 4104), ([1], 4104, 136), ([33], 72, 2056), ([5, 64, 0, 31], 776, 904), ([200], 648, 776), ([7, 9], 392, 520),
+], ids=lambda v: "-".join(map(str, v)) if isinstance(v, list) else str(v))
+@pytest.mark.parametrize("out", [F32, BF])
+def test_few_tiles_of_long_sums_exact(dev, counts, N, K, out):
+    run_all(counts, 2, N, K, BF, out, dev, seed=17)
+
+
 def test_large_tiles_of_normal_values(dev):
     run_all([1500, 0, 17, 2579], 3, 2056, 520, BF, BF, dev, seed=13, make=normal, exact=False)
     run_all([1300, 900, 0, 1900], 0, 520, 2056, BF, F32, dev, seed=14, make=normal, exact=False)
