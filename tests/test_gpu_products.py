@@ -277,6 +277,16 @@ def test_few_tiles_of_long_sums_exact(dev, counts, N, K, out):
     run_all(counts, 2, N, K, BF, out, dev, seed=17)
 
 
+# fp32: 16 x 64 tiles with the contraction whole and split in four, 64 x 64 ones whole and split in two
+@pytest.mark.parametrize("counts,N,K", [
+    ([20] * 40 + [0, 47], 1160, 1160), ([3, 0, 1] * 20, 1032, 264), ([26], 3800, 104), ([300, 0, 517, 100], 1032, 1160),
+    ([900, 0, 1300, 700], 1032, 1160),
+], ids=["16-rows", "16-rows-split", "16-rows-split-long", "64-rows-split", "64-rows"])
+@pytest.mark.parametrize("out", [F32, BF])
+def test_every_fp32_tile_exact(dev, counts, N, K, out):
+    run_all(counts, 3, N, K, F32, out, dev, seed=18)
+
+
 def test_large_tiles_of_normal_values(dev):
     run_all([1500, 0, 17, 2579], 3, 2056, 520, BF, BF, dev, seed=13, make=normal, exact=False)
     run_all([1300, 900, 0, 1900], 0, 520, 2056, BF, F32, dev, seed=14, make=normal, exact=False)

@@ -198,18 +198,18 @@ __device__ __forceinline__ bool tile_at(const ProductArgs& p, int TM, int TN, Ti
   return true;
 }
 
-// One operand of one step: TM rows (along) or columns (across) of C's side, 32 of the
-// contraction. base: the operand's first element of the tile; lim: rows or columns of the tile
+// One operand of one step: TM rows (along) or columns (across) of C's side, KD of the
+// contraction, by NT threads. base: the operand's first element of the tile; lim: rows or columns of the tile
 // that exist; ld: its row stride; k0, kdim: the step's first contraction element and their
 // number. What lies outside reads as zero.
-template <bool ACROSS, int TM>
+template <bool ACROSS, int TM, int KD, int NT>
 struct Stage {
-  static constexpr int kAll = TM * kStep / 4;          // 4-element chunks
-  static constexpr int NCH = (kAll + 255) / 256;       // per thread
+  static constexpr int kAll = TM * KD / 4;             // 4-element chunks
+  static constexpr int NCH = (kAll + NT - 1) / NT;     // per thread
   float4 c[NCH];
   __device__ __forceinline__ static void at(int i, int& outer, int& inner) {
-    const int q = threadIdx.x + i * 256;
-    constexpr int per = (ACROSS ? TM : kStep) / 4;  // chunks per LDS row
+    const int q = threadIdx.x + i * NT;
+    constexpr int per = (ACROSS ? TM : KD) / 4;  // chunks per LDS row
     outer = q / per;
     inner = q % per * 4;
   }
@@ -218,49 +218,54 @@ struct Stage {
     for (int i = 0; i < NCH; ++i) {
       int o, n;
       at(i, o, n);
-      const bool ok = (kAll % 256 == 0 || (int)threadIdx.x + i * 256 < kAll) &&
+      const bool ok = (kAll % NT == 0 || (int)threadIdx.x + i * NT < kAll) &&
                       (ACROSS ? (k0 + o < kdim && n < lim) : (o < lim && k0 + n < kdim));
       const size_t e = ACROSS ? (size_t)(k0 + o) * ld + n : (size_t)o * ld + k0 + n;
       c[i] = ok ? *reinterpret_cast<const float4*>(base + e) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
   }
   __device__ __forceinline__ void put(float* lds) const {
-    constexpr int row = (ACROSS ? TM : kStep) + kPad;
+    constexpr int row = (ACROSS ? TM : KD) + kPad;
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
       int o, n;
       at(i, o, n);
-      if (kAll % 256 == 0 || (int)threadIdx.x + i * 256 < kAll) *reinterpret_cast<float4*>(lds + o * row + n) = c[i];
+      if (kAll % NT == 0 || (int)threadIdx.x + i * NT < kAll) *reinterpret_cast<float4*>(lds + o * row + n) = c[i];
     }
   }
 };
 
-template <bool ACROSS, int TM>
+template <bool ACROSS, int TM, int KD>
 __device__ __forceinline__ f32x4 fragment(const float* lds, int m, int k) {
   if constexpr (ACROSS) {
     const float* s = lds + k * (TM + kPad) + m;
     return f32x4{s[0], s[TM + kPad], s[2 * (TM + kPad)], s[3 * (TM + kPad)]};
   } else {
-    const float4 v = *reinterpret_cast<const float4*>(lds + m * (kStep + kPad) + k);
+    const float4 v = *reinterpret_cast<const float4*>(lds + m * (KD + kPad) + k);
     return f32x4{v.x, v.y, v.z, v.w};
   }
 }
 
-template <bool ACROSS, int TM>
-constexpr int stage_floats() { return ACROSS ? kStep * (TM + kPad) : TM * (kStep + kPad); }
+template <bool ACROSS, int TM, int KD>
+constexpr int stage_floats() { return ACROSS ? KD * (TM + kPad) : TM * (KD + kPad); }
 
-template <GroupedProduct P, int FM, int FN, int WGM>
-__global__ __launch_bounds__(256) void f32_kernel(ProductArgs p) {
+// KS: groups of 4 waves, each of which takes 32 of a step's KS * 32 contraction elements; their sums
+// are joined at the end, in order.
+template <GroupedProduct P, int FM, int FN, int WGM, int KS>
+__global__ __launch_bounds__(256 * KS) void f32_kernel(ProductArgs p) {
   constexpr bool AX = P == kWgrad, BX = P != kForward;
   constexpr int WGN = 4 / WGM, TM = 16 * FM * WGM, TN = 16 * FN * WGN;
-  __shared__ __align__(16) float la[stage_floats<AX, TM>()];
-  __shared__ __align__(16) float lb[stage_floats<BX, TN>()];
+  constexpr int KD = kStep * KS, NT = 256 * KS;
+  constexpr int kA = stage_floats<AX, TM, KD>(), kB = stage_floats<BX, TN, KD>();
+  __shared__ __align__(16) float lds[kA + kB];
+  float *const la = lds, *const lb = lds + kA;
   TileAt t;
   if (!tile_at<P, false>(p, TM, TN, t)) return;
   const int e = t.e, ra = t.ra, m0 = t.m0, c0 = t.c0, mlim = t.mlim, clim = t.clim, kdim = t.kdim;
   const int cols = P == kForward ? p.N : p.K;
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) & 3;
+  const int group = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
   const int wm = wave % WGM, wn = wave / WGM;
   const int lda = P == kForward ? p.K : p.N;
   const size_t wbase = (size_t)e * p.N * p.K;
@@ -277,13 +282,13 @@ __global__ __launch_bounds__(256) void f32_kernel(ProductArgs p) {
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = sum[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  const int steps1 = (kdim + kStep - 1) / kStep;
+  const int steps1 = (kdim + KD - 1) / KD;
   const int steps = (P == kDgrad && p.a2) ? 2 * steps1 : steps1;
-  Stage<AX, TM> sa;
-  Stage<BX, TN> sb;
+  Stage<AX, TM, KD, NT> sa;
+  Stage<BX, TN, KD, NT> sb;
   auto load = [&](int st) __attribute__((always_inline)) {
     const bool second = st >= steps1;
-    const int k0 = (second ? st - steps1 : st) * kStep;
+    const int k0 = (second ? st - steps1 : st) * KD;
     sa.load(static_cast<const float*>(second ? p.a2 : p.a) + a_at, mlim, lda, k0, kdim);
     sb.load(static_cast<const float*>(second ? p.b2 : p.b) + b_at, clim, p.K, k0, kdim);
   };
@@ -296,12 +301,12 @@ __global__ __launch_bounds__(256) void f32_kernel(ProductArgs p) {
     if (st + 1 < steps) load(st + 1);  // in flight under the products
 #pragma unroll
     for (int s = 0; s < kStep / 16; ++s) {
-      const int k = s * 16 + (lane >> 4) * 4;
+      const int k = group * kStep + s * 16 + (lane >> 4) * 4;
       f32x4 fa[FM], fb[FN];
 #pragma unroll
-      for (int i = 0; i < FM; ++i) fa[i] = fragment<AX, TM>(la, (wm * FM + i) * 16 + (lane & 15), k);
+      for (int i = 0; i < FM; ++i) fa[i] = fragment<AX, TM, KD>(la, (wm * FM + i) * 16 + (lane & 15), k);
 #pragma unroll
-      for (int j = 0; j < FN; ++j) fb[j] = fragment<BX, TN>(lb, (wn * FN + j) * 16 + (lane & 15), k);
+      for (int j = 0; j < FN; ++j) fb[j] = fragment<BX, TN, KD>(lb, (wn * FN + j) * 16 + (lane & 15), k);
 #pragma unroll
       for (int q = 0; q < 4; ++q)
 #pragma unroll
@@ -319,6 +324,26 @@ __global__ __launch_bounds__(256) void f32_kernel(ProductArgs p) {
           acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
     }
+  }
+  if constexpr (KS > 1) {
+    static_assert((KS - 1) * FM * FN * 1024 <= kA + kB, "the groups' sums fit where the operands were");
+    __syncthreads();
+    float* const mine = lds + ((group - 1) * FM * FN * 4 + wave) * 256 + lane * 4;
+    if (group > 0) {
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) *reinterpret_cast<f32x4*>(mine + (i * FN + j) * 1024) = sum[i][j];
+    }
+    __syncthreads();
+    if (group > 0) return;
+#pragma unroll
+    for (int g = 0; g < KS - 1; ++g)
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+          sum[i][j] += *reinterpret_cast<const f32x4*>(lds + ((g * FM * FN + i * FN + j) * 4 + wave) * 256 + lane * 4);
   }
   OutTile o;
   o.set(p, P == kWgrad ? (size_t)e * p.N + m0 : (size_t)ra + m0, mlim, c0, clim, cols);
@@ -603,10 +628,10 @@ hipError_t launch_tiles(const GroupedGemmArgs& a, const ProductArgs& p, hipStrea
   return hipGetLastError();
 }
 
-template <GroupedProduct P, int FM, int FN, int WGM>
+template <GroupedProduct P, int FM, int FN, int WGM, int KS>
 hipError_t launch_f32(const GroupedGemmArgs& a, const ProductArgs& p, hipStream_t stream) {
   const long long grid = xcd_grid(tile_items(P, a, 16 * FM * WGM, 16 * FN * (4 / WGM)));
-  f32_kernel<P, FM, FN, WGM><<<(unsigned)grid, 256, 0, stream>>>(p);
+  f32_kernel<P, FM, FN, WGM, KS><<<(unsigned)grid, 256 * KS, 0, stream>>>(p);
   return hipGetLastError();
 }
 
@@ -658,9 +683,19 @@ hipError_t launch_product(const GroupedGemmArgs& a, int cus, hipStream_t stream)
   if (!a.bf16) {
     // Few rows leave most of a 64-row tile's products empty: at 64 experts of 1024 x 2048, even rows,
     // tiles of 16 x 64 against 64 x 64 took (forward) 124 and 166 us at 1 row per expert, 128 and
-    // 165 at 32, 235 and 180 at 64.
-    if (P != kWgrad && a.rows / a.E < 48) return launch_f32<P, 1, 1, 1>(a, p, stream);
-    return launch_f32<P, 2, 2, 2>(a, p, stream);
+    // 165 at 32, 235 and 180 at 64. The contraction is split over the waves where there are few tiles
+    // (one expert of 1024 x 1024, 512 rows, forward: 31 us in tiles of 64 x 64, 27 split in two, 22 in tiles of
+    // 16 x 64 split in four; 4 experts, 1,024 rows, input gradients 35, 28 and 39) or one row tile per
+    // expert (the 64 experts at 1 row 96 us against 124); at 32 rows each it costs (145 against 134).
+    if constexpr (P == kWgrad) {
+      return launch_f32<P, 2, 2, 2, 1>(a, p, stream);
+    } else {
+      if (a.rows / a.E < 16 || tile_items(P, a, 16, 64) <= 5LL * cus / 2)
+        return launch_f32<P, 1, 1, 1, 4>(a, p, stream);
+      if (a.rows / a.E < 48) return launch_f32<P, 1, 1, 1, 1>(a, p, stream);
+      if (tile_items(P, a, 64, 64) <= 2LL * cus) return launch_f32<P, 2, 2, 2, 2>(a, p, stream);
+      return launch_f32<P, 2, 2, 2, 1>(a, p, stream);
+    }
   }
   // Which tiles, from the sizes alone (the host does not know the offsets). Measured at 64 experts of
   // 2048 x 4096, rows spread evenly (us):
@@ -692,10 +727,11 @@ hipError_t launch_product(const GroupedGemmArgs& a, int cus, hipStream_t stream)
     // With a CU to each tile, small tiles and as many steps in flight as the LDS holds: one expert of
     // 1024 x 2048, forward, 256 rows 10.4 us against 18.7 in tiles of 64 x 128, 512 rows 11.7 against 18.5,
     // 768 rows (384 tiles) 19.4 against 18.7; one token for 8 of 128 experts of 1536 x 4096 17.9 against
-    // 18.5 in the three-slot rings; the input gradient of two with 2048 x 1024, 256 rows 32.9 against 41.7.
+    // 18.5 in the three-slot rings; input gradients of two with 2048 x 1024, 512 rows over 8 experts 22 against
+    // 42 (34 in steps of 64, whose waits and barriers then take most of the time).
     if (few_tiles(P, a, P == kForward ? 64 : 128, cus)) {
       if constexpr (P == kForward) return launch_tiles<P, 32, 16, 1, 4, 128, 6, true, false>(a, p, stream);
-      return launch_tiles<P, 32, 32, 1, 4, 64, 7, true, false>(a, p, stream);
+      return launch_tiles<P, 32, 16, 1, 8, 128, 3, true, false>(a, p, stream);
     }
     if (mean >= 96) {
       const double small = step_time(P, a, kSmall, cus);
@@ -712,13 +748,13 @@ hipError_t launch_product(const GroupedGemmArgs& a, int cus, hipStream_t stream)
 }  // namespace
 
 bool grouped_gemm_fits(const GroupedGemmArgs& a, GroupedProduct kind) {
-  // the smallest tiles that launch_product may take
+  // the smallest tiles that launch_product may take (but where it takes them for being few)
   const long long mean = a.rows / a.E;
-  int TM = 64, TN = 64;
+  int TM = 64, TN = 64, threads = 256;
   if (kind == kWgrad) TM = TN = a.bf16 ? 128 : 64;
   else if (a.bf16) TM = mean >= 12 ? 64 : 32, TN = mean >= 12 ? 128 : 64;
-  else if (mean < 48) TM = 16;
-  return xcd_grid(tile_items(kind, a, TM, TN)) <= kMaxWorkgroups;
+  else if (mean < 48) TM = 16, threads = mean < 16 ? 1024 : 256;
+  return xcd_grid(tile_items(kind, a, TM, TN)) <= kMaxWorkgroups * 256 / threads;
 }
 
 hipError_t launch_grouped_gemm(const GroupedGemmArgs& a, GroupedProduct kind, hipStream_t stream) {
