@@ -268,9 +268,11 @@ def test_every_tile_size_exact(dev, counts, N, K, out):
     run_all(counts, 3, N, K, BF, out, dev, seed=12)
 
 
-# Few tiles, each with a CU of its own and more steps than the ring has slots, or fewer, or a part of one
+# Few tiles, each with a CU of its own (of 32, 64 and 128 rows), with more steps than the ring has slots, fewer, or a
+# part of one; and one case of tiles of 64 rows past that
 @pytest.mark.parametrize("counts,N,K", [
     ([40, 0, 3], 1544, 4104), ([1], 4104, 136), ([33], 72, 2056), ([5, 64, 0, 31], 776, 904), ([200], 648, 776), ([7, 9], 392, 520),
+    ([300, 500, 0, 900, 260], 1160, 1160), ([30, 0, 55, 70] * 5, 520, 776), ([30, 0, 55, 70] * 8, 2056, 2056), ([1900], 264, 392),
 ], ids=lambda v: "-".join(map(str, v)) if isinstance(v, list) else str(v))
 @pytest.mark.parametrize("out", [F32, BF])
 def test_few_tiles_of_long_sums_exact(dev, counts, N, K, out):

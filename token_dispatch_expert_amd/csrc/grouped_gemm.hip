@@ -635,11 +635,19 @@ hipError_t launch_f32(const GroupedGemmArgs& a, const ProductArgs& p, hipStream_
   return hipGetLastError();
 }
 
+// How many of them to expect; with several experts, each one's last row tile is taken to be half full.
+double expected_tiles(GroupedProduct kind, const GroupedGemmArgs& a, int TM, int TN) {
+  const double active = a.E < a.rows ? a.E : a.rows;
+  const double rows = kind == kWgrad ? a.E * std::ceil(a.N / (double)TM)
+                      : a.E == 1     ? std::ceil(a.rows / (double)TM)
+                                     : std::fmax(a.rows / (double)TM + 0.5 * active, active);
+  return rows * std::ceil((kind == kForward ? a.N : a.K) / (double)TN);
+}
+
 // Time, per contraction step of 64 (us), of TM x TN tiles over the CUs, `fit` to each at a time: `full`
-// where the CUs are filled, `alone` for a last round with at most one tile to a CU. With several
-// experts, each one's last row tile is taken to be half full. The times are from products of 512
-// to 8192 rows over 1 to 16 experts (forward, 1024 rows of 2048 x 7168 for one expert: 136 us in
-// tiles of 256, 78 of 128, 59 of 64 x 128; 4096 rows of 4096 x 1024 for 8 experts: 33, 43 and 55).
+// where the CUs are filled, `alone` for a last round with at most one tile to a CU. The times are from
+// products of 512 to 8192 rows over 1 to 16 experts (forward, 1024 rows of 2048 x 7168 for one expert:
+// 136 us in tiles of 256, 78 of 128, 59 of 64 x 128; 4096 rows of 4096 x 1024 for 8 experts: 33, 43 and 55).
 struct TileCost {
   int TM, TN, fit;
   double alone, full;
@@ -647,11 +655,7 @@ struct TileCost {
 constexpr TileCost kBig{256, 256, 1, 1.3, 1.3}, kMid{128, 128, 2, 0.7, 1.05}, kSmall{64, 128, 2, 0.48, 0.75};
 
 double step_time(GroupedProduct kind, const GroupedGemmArgs& a, const TileCost& c, int cus) {
-  const double active = a.E < a.rows ? a.E : a.rows;
-  double tiles = kind == kWgrad ? a.E * std::ceil(a.N / (double)c.TM)
-                 : a.E == 1     ? std::ceil(a.rows / (double)c.TM)
-                                : std::fmax(a.rows / (double)c.TM + 0.5 * active, active);
-  tiles *= std::ceil((kind == kForward ? a.N : a.K) / (double)c.TN);
+  const double tiles = expected_tiles(kind, a, c.TM, c.TN);
   const double slots = (double)cus * c.fit, whole = std::floor(tiles / slots), left = tiles - whole * slots;
   return whole * c.full + (left == 0 ? 0 : left <= cus ? c.alone : c.full);
 }
@@ -667,13 +671,6 @@ int stream_rows(const GroupedGemmArgs& a, GroupedProduct kind) {
   if (cols * (a.out_bf16 ? 2 : 4) % 128 == 0) return 1;
   if (kind == kWgrad) return a.rows / a.E >= (a.out_bf16 ? 192 : 512);
   return (kind == kForward ? a.K : a.N) >= 4096;
-}
-
-// Tiles of 32 rows that leave a CU to each (of one expert: exactly; of several: tile_items counts one
-// that may be partial for each).
-bool few_tiles(GroupedProduct kind, const GroupedGemmArgs& a, int TN, int cus) {
-  if (a.E > 1) return 2 * tile_items(kind, a, 32, TN) <= 3LL * cus;
-  return (a.rows + 31LL) / 32 * (((kind == kForward ? a.N : a.K) + TN - 1LL) / TN) <= cus;
 }
 
 template <GroupedProduct P>
@@ -722,17 +719,27 @@ hipError_t launch_product(const GroupedGemmArgs& a, int cus, hipStream_t stream)
   if constexpr (P == kWgrad) {
     if (mean >= (a.out_bf16 ? 16 : 160) && a.N > 128 && a.K > 128 && big <= mid)
       return launch_tiles<P, 128, 64, 2, 4, 64, 2, false, true>(a, p, stream);
+    // With a CU to each tile, eight waves and steps of 128: one expert of 1024 x 1024, 8,192 rows 63 us
+    // against 91.
+    if (expected_tiles(P, a, 128, 128) <= cus)
+      return launch_tiles<P, 64, 32, 2, 4, 128, 2, false, false>(a, p, stream);
     return launch_tiles<P, 64, 64, 2, 2, 64, 2, false, false>(a, p, stream);
   } else {
-    // With a CU to each tile, small tiles and as many steps in flight as the LDS holds: one expert of
-    // 1024 x 2048, forward, 256 rows 10.4 us against 18.7 in tiles of 64 x 128, 512 rows 11.7 against 18.5,
-    // 768 rows (384 tiles) 19.4 against 18.7; one token for 8 of 128 experts of 1536 x 4096 17.9 against
-    // 18.5 in the three-slot rings; input gradients of two with 2048 x 1024, 512 rows over 8 experts 22 against
-    // 42 (34 in steps of 64, whose waits and barriers then take most of the time).
-    if (few_tiles(P, a, P == kForward ? 64 : 128, cus)) {
-      if constexpr (P == kForward) return launch_tiles<P, 32, 16, 1, 4, 128, 6, true, false>(a, p, stream);
-      return launch_tiles<P, 32, 16, 1, 8, 128, 3, true, false>(a, p, stream);
+    // With a CU to each tile, the smallest tiles of which that is so, with as many steps in flight as the
+    // LDS holds, eight waves and steps of 128 (in steps of 64 their waits and barriers take most of the
+    // time). One expert of 1024 x 2048, forward: 256 rows 10.4 us in tiles of 32 x 64 against 18.7 in the
+    // three-slot tiles of 64 x 128; 1,024 rows 14.6 in these tiles of 64 x 128 against 18.7; 4,096 rows 23.5
+    // in these of 128 against 27.2 in the ones for full CUs. Input gradients of two with 1024 x 2048: 1,536
+    // rows 27.6 against 41.4, 4,096 rows 39.9 against 53.7. One token for 8 of 128 experts of 1536 x 4096
+    // 17.9 against 18.5.
+    const auto few = [&](int TM, int TN) { return expected_tiles(P, a, TM, TN) <= cus; };
+    if constexpr (P == kForward) {
+      if (few(32, 64)) return launch_tiles<P, 32, 16, 1, 4, 128, 6, true, false>(a, p, stream);
+    } else {
+      if (few(32, 128)) return launch_tiles<P, 32, 16, 1, 8, 128, 3, true, false>(a, p, stream);
     }
+    if (few(64, 128)) return launch_tiles<P, 32, 32, 2, 4, 128, 3, true, false>(a, p, stream);
+    if (few(128, 128)) return launch_tiles<P, 64, 32, 2, 4, 128, 2, true, false>(a, p, stream);
     if (mean >= 96) {
       const double small = step_time(P, a, kSmall, cus);
       if (mean >= (P == kForward ? 192 : 96) && (P == kForward ? a.N : a.K) > 128 && big <= mid && big <= small)
