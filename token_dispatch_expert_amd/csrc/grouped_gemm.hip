@@ -198,40 +198,48 @@ __device__ __forceinline__ bool tile_at(const ProductArgs& p, int TM, int TN, Ti
   return true;
 }
 
-// One operand of one step: TM rows (along) or columns (across) of C's side, KD of the
-// contraction, by NT threads. base: the operand's first element of the tile; lim: rows or columns of the tile
-// that exist; ld: its row stride; k0, kdim: the step's first contraction element and their
-// number. What lies outside reads as zero.
+// One operand: TM rows (along) or columns (across) of C's side, KD of the contraction per step, loaded
+// by NT threads in 16-byte chunks. Loads go through a buffer descriptor that ends with the last row that
+// exists, so that what lies outside reads as zero and a step needs hardly any address arithmetic. (An
+// across operand's columns past the matrix read what is there: they meet only columns or rows of C that
+// do not exist either.)
 template <bool ACROSS, int TM, int KD, int NT>
 struct Stage {
-  static constexpr int kAll = TM * KD / 4;             // 4-element chunks
-  static constexpr int NCH = (kAll + NT - 1) / NT;     // per thread
-  float4 c[NCH];
-  __device__ __forceinline__ static void at(int i, int& outer, int& inner) {
-    const int q = threadIdx.x + i * NT;
-    constexpr int per = (ACROSS ? TM : KD) / 4;  // chunks per LDS row
-    outer = q / per;
-    inner = q % per * 4;
+  static constexpr int kAll = TM * KD / 4;              // chunks
+  static constexpr int NCH = (kAll + NT - 1) / NT;      // per thread
+  static constexpr int kRowChunks = (ACROSS ? TM : KD) / 4;
+  static constexpr int kRow = (ACROSS ? TM : KD) + kPad;  // floats of an LDS row
+  static constexpr int kOutside = 0x40000000;           // past any extent (at most 128 * 2^22 bytes)
+  static_assert(NT % kRowChunks == 0, "a thread's chunks lie in one column");
+  u32x4 c[NCH];
+  const char* base;
+  int ld, extent, lane_at, inner;
+
+  // base_: the operand's first element of the tile; count: its rows that exist (along) or the columns
+  // before it in a row (across); ld_elems: row stride
+  __device__ __forceinline__ void set(const float* base_, int count, int ld_elems) {
+    base = reinterpret_cast<const char*>(base_);
+    ld = ld_elems * 4;
+    inner = (int)threadIdx.x % kRowChunks * 4;
+    lane_at = (int)threadIdx.x / kRowChunks * ld + inner * 4;
+    if (kAll < NT && (int)threadIdx.x >= kAll) lane_at = kOutside;
+    extent = ACROSS ? -count * 4 : count * ld;
   }
-  __device__ __forceinline__ void load(const float* base, int lim, int ld, int k0, int kdim) {
+  // contraction elements from k0 (kdim in all); moved: bytes to the operand of the second pair
+  __device__ __forceinline__ void load(int k0, int kdim, ptrdiff_t moved) {
+    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)(base + moved + (ACROSS ? (ptrdiff_t)k0 * ld : 0)), (short)0,
+        ACROSS ? min(KD, kdim - k0) * ld + extent : extent, kBufferWord3);
+    const int at = ACROSS || inner < kdim - k0 ? lane_at : kOutside;
 #pragma unroll
-    for (int i = 0; i < NCH; ++i) {
-      int o, n;
-      at(i, o, n);
-      const bool ok = (kAll % NT == 0 || (int)threadIdx.x + i * NT < kAll) &&
-                      (ACROSS ? (k0 + o < kdim && n < lim) : (o < lim && k0 + n < kdim));
-      const size_t e = ACROSS ? (size_t)(k0 + o) * ld + n : (size_t)o * ld + k0 + n;
-      c[i] = ok ? *reinterpret_cast<const float4*>(base + e) : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
+    for (int i = 0; i < NCH; ++i)
+      c[i] = __builtin_amdgcn_raw_buffer_load_b128(r, at + i * (NT / kRowChunks) * ld, ACROSS ? 0 : k0 * 4, 0);
   }
   __device__ __forceinline__ void put(float* lds) const {
-    constexpr int row = (ACROSS ? TM : KD) + kPad;
 #pragma unroll
-    for (int i = 0; i < NCH; ++i) {
-      int o, n;
-      at(i, o, n);
-      if (kAll % NT == 0 || (int)threadIdx.x + i * NT < kAll) *reinterpret_cast<float4*>(lds + o * row + n) = c[i];
-    }
+    for (int i = 0; i < NCH; ++i)
+      if (kAll % NT == 0 || (int)threadIdx.x + i * NT < kAll)
+        *reinterpret_cast<u32x4*>(lds + ((int)threadIdx.x / kRowChunks + i * (NT / kRowChunks)) * kRow + inner) = c[i];
   }
 };
 
@@ -286,11 +294,16 @@ __global__ __launch_bounds__(256 * KS) void f32_kernel(ProductArgs p) {
   const int steps = (P == kDgrad && p.a2) ? 2 * steps1 : steps1;
   Stage<AX, TM, KD, NT> sa;
   Stage<BX, TN, KD, NT> sb;
+  sa.set(static_cast<const float*>(p.a) + a_at, AX ? m0 : mlim, lda);
+  sb.set(static_cast<const float*>(p.b) + b_at, BX ? c0 : clim, p.K);
+  const bool pair = P == kDgrad && p.a2;
+  const ptrdiff_t moved_a = pair ? static_cast<const char*>(p.a2) - static_cast<const char*>(p.a) : 0;
+  const ptrdiff_t moved_b = pair ? static_cast<const char*>(p.b2) - static_cast<const char*>(p.b) : 0;
   auto load = [&](int st) __attribute__((always_inline)) {
     const bool second = st >= steps1;
     const int k0 = (second ? st - steps1 : st) * KD;
-    sa.load(static_cast<const float*>(second ? p.a2 : p.a) + a_at, mlim, lda, k0, kdim);
-    sb.load(static_cast<const float*>(second ? p.b2 : p.b) + b_at, clim, p.K, k0, kdim);
+    sa.load(k0, kdim, second ? moved_a : 0);
+    sb.load(k0, kdim, second ? moved_b : 0);
   };
   if (steps > 0) load(0);
   for (int st = 0; st < steps; ++st) {
