@@ -282,8 +282,8 @@ def test_few_tiles_of_long_sums_exact(dev, counts, N, K, out):
 # fp32: 16 x 64 tiles with the contraction whole and split in four, 64 x 64 ones whole and split in two
 @pytest.mark.parametrize("counts,N,K", [
     ([20] * 40 + [0, 47], 1160, 1160), ([3, 0, 1] * 20, 1032, 264), ([26], 3800, 104), ([300, 0, 517, 100], 1032, 1160),
-    ([900, 0, 1300, 700], 1032, 1160),
-], ids=["16-rows", "16-rows-split", "16-rows-split-long", "64-rows-split", "64-rows"])
+    ([900, 0, 1300, 700], 1032, 1160), ([700, 0, 333], 264, 392),
+], ids=["16-rows", "16-rows-split", "16-rows-split-long", "64-rows-split", "64-rows", "wgrad-split"])
 @pytest.mark.parametrize("out", [F32, BF])
 def test_every_fp32_tile_exact(dev, counts, N, K, out):
     run_all(counts, 3, N, K, F32, out, dev, seed=18)

@@ -32,9 +32,11 @@ namespace {
 // lane (row or column lane % 16, element lane / 16); lane group g takes elements 4g .. 4g + 3
 // of a 16-long slice in turn, the same for both operands, so an along fragment is one 16-byte
 // read. The operands go in as (B, A), which gives each lane 4 consecutive columns of one row of C.
-// Bound by the matrix instructions: 16,384 rows over 8 experts of 1024 x 2048 take 634 us forward
-// (108 TFLOP/s; a large fp32 library product reaches 132), 1.21 ms for two input gradients, 617 us
-// for the weight gradient. Tiles of 128 measured slower at every size (693, 1380 and 736 us).
+// Bound by the matrix instructions: 16,384 rows over 8 experts of 1024 x 2048 take 547 us forward
+// (126 TFLOP/s; a large fp32 library product reaches 132), 1.09 ms for two input gradients, 542 us
+// for the weight gradient. Tiles of 128 measured slower at every size, by 9 to 19%. With few tiles it
+// is the chain of a step that bounds (LDS, barriers, dependent products); two to four steps' loads
+// ahead gained nothing there.
 constexpr int kStep = 32;
 constexpr int kPad = 4;
 
@@ -698,6 +700,8 @@ hipError_t launch_product(const GroupedGemmArgs& a, int cus, hipStream_t stream)
     // 16 x 64 split in four; 4 experts, 1,024 rows, input gradients 35, 28 and 39) or one row tile per
     // expert (the 64 experts at 1 row 96 us against 124); at 32 rows each it costs (145 against 134).
     if constexpr (P == kWgrad) {
+      // few tiles of many rows: one expert of 1024 x 1024, 4,096 rows 87 us against 113
+      if (a.rows / a.E >= 128 && expected_tiles(P, a, 64, 64) <= cus) return launch_f32<P, 2, 2, 2, 2>(a, p, stream);
       return launch_f32<P, 2, 2, 2, 1>(a, p, stream);
     } else {
       if (a.rows / a.E < 16 || tile_items(P, a, 16, 64) <= 5LL * cus / 2)
