@@ -114,6 +114,9 @@ def test_binding_refuses_wrong_tensors():
         (TypeError, moe.moe_checkpoint_unpack, (z(4, 16, t=f8), z(4, 1, t=f32), z(4, 16, t=torch.float16)), {}),
         (ValueError, moe.moe_swiglu, (z(4, 16), z(4, 16), z(4, 16)), dict(g_codes=z(4, 16, t=f8))),
         (ValueError, moe.moe_swiglu_backward, (z(4, 16), z(4, 16), z(4, 16), z(4, 16), z(4, 16)), dict(g_scales=z(4, 1, t=f32))),
+        (ValueError, moe.moe_swiglu, (z(4, 16), z(4, 16), z(4, 16)), dict(offsets=i(0))),                # of no expert
+        (ValueError, moe.moe_swiglu, (z(4, 16), z(4, 16), z(4, 16)), dict(offsets=i(1))),
+        (ValueError, moe.moe_swiglu, (z(4, 16), z(4, 16), z(4, 16)), dict(offsets=i(4).reshape(2, 2))),
         (TypeError, moe.moe_swiglu_backward, (z(4, 16), z(4, 16, t=f32), z(4, 16, t=f32), z(4, 16), z(4, 16)), {}),
         (ValueError, moe.moe_combine_backward, (z(4, 16), None, i(8), z(4, 2, t=f32), z(8, 16), z(4, 2, t=f32)), {}),
         (ValueError, moe.moe_permute_backward, (z(8, 16), i(8), 3, z(4, 16)), {}),

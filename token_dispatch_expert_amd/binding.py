@@ -502,9 +502,11 @@ def moe_swiglu(g, u, h, g_codes=None, g_scales=None, u_codes=None, u_scales=None
 def _row_offsets(offsets) -> int:
     if offsets is None:
         return 0
-    E, = _dims(offsets, 1, "offsets")
-    _need(offsets, torch.int32, (E,), "offsets")
-    return E - 1
+    n, = _dims(offsets, 1, "offsets")
+    _need(offsets, torch.int32, (n,), "offsets")
+    if n < 2:  # (an empty tensor's address is NULL, which means all rows)
+        raise ValueError("offsets: expected E + 1 entries")
+    return n - 1
 
 
 def moe_swiglu_backward(dh, g, u, dg, du, h=None, g_scales=None, u_scales=None, offsets=None, stream=None):
