@@ -428,6 +428,74 @@ def test_training_step_captured_and_replayed(dev, T, E, k, d, f, dtype):
                 assert torch.equal(got[n], s.b[n]), (rep, i, n)
 
 
+def test_two_training_steps_at_once(dev):
+    """Two steps of their own tensors, their calls dealt in turn to two streams, against the same steps alone."""
+    names = ("y", "dx", "dlogits", "dwg", "dwu", "dwd")
+    steps = [Step(700, 16, 4, 256, 384, BF, dev, held=True, seed=1), Step(90, 8, 2, 136, 264, F32, dev, held=True, seed=2)]
+    alone = []
+    for s in steps:
+        s.forward(), s.backward()
+        torch.cuda.synchronize()
+        alone.append({n: s.b[n].clone() for n in names})
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for rep in range(3):
+        for s in steps:
+            for n in names:
+                s.b[n].fill_(float("nan"))
+        torch.cuda.synchronize()
+        for part in ("forward", "backward"):
+            for s, stream in zip(steps, streams):
+                with torch.cuda.stream(stream):
+                    getattr(s, part)()
+        torch.cuda.synchronize()
+        for s, want in zip(steps, alone):
+            for n in names:
+                assert torch.equal(s.b[n], want[n]), (rep, n)
+
+
+def test_calls_run_on_the_stream_they_are_given(dev):
+    """Inputs arrive late on a side stream that is not the current one; only calls on that stream see them."""
+    T, E, k, d = 200, 8, 2, 264
+    R, side = T * k, torch.cuda.Stream()
+    f2s = torch.randperm(R, generator=torch.Generator().manual_seed(3)).to(dev, torch.int32)
+    off = ref.offsets_of([R // E] * E, dev)
+    gates, ids = torch.rand((T, k), device=dev), torch.arange(R, device=dev).reshape(T, k).remainder(E).to(torch.int32)
+    late = {n: normal(shape, 40 + i, dev) for i, (n, shape) in enumerate(dict(x=(T, d), r=(R, d), q=(R, d), g=(T, k), w=(E, d, d)).items())}
+    slow = torch.zeros((4096, 4096), device=dev)
+
+    def run(t, stream):
+        z = lambda *s, t=F32: torch.empty(s, dtype=t, device=dev)  # noqa: E731
+        held = lambda n: (z(n, d, t=F8), z(n, -(-d // 128)))  # noqa: E731
+        o = dict(xc=held(T), up=z(R, d), gc=held(R), uc=held(R), h=z(R, d), dg=z(R, d), du=z(R, d), dys=z(R, d), dgates=z(T, k),
+                 dx=z(T, d), dl=z(T, E), y=z(R, d), dxs=z(R, d), dw=z(E, d, d))
+        torch.cuda.current_stream().synchronize()  # the buffers' earlier uses are over
+        moe.moe_checkpoint_pack(t["x"], *o["xc"], stream=stream)
+        moe.moe_checkpoint_unpack(*o["xc"], o["up"], flat_to_sorted=f2s, stream=stream)
+        moe.moe_swiglu(t["r"], t["q"], o["h"], *o["gc"], *o["uc"], stream=stream)
+        moe.moe_swiglu_backward(t["q"], o["gc"][0], o["uc"][0], o["dg"], o["du"], g_scales=o["gc"][1], u_scales=o["uc"][1], stream=stream)
+        moe.moe_combine_backward(t["x"], t["r"], f2s, gates, o["dys"], o["dgates"], stream=stream)
+        moe.moe_permute_backward(t["r"], f2s, k, o["dx"], stream=stream)
+        moe.moe_route_backward(t["g"], ids, gates, o["dl"], stream=stream)
+        moe.moe_grouped_gemm(t["r"], off, t["w"], o["y"], stream=stream)
+        moe.moe_grouped_gemm_dgrad(t["r"], off, t["w"], o["dxs"], stream=stream)
+        moe.moe_grouped_gemm_wgrad(t["r"], t["q"], off, o["dw"], stream=stream)
+        return o
+    want = run(late, None)
+    torch.cuda.synchronize()
+    t = {n: torch.zeros_like(v) for n, v in late.items()}
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(20):
+            slow.addmm_(slow, slow)
+        for n, v in t.items():
+            v.copy_(late[n])
+    got = run(t, side)
+    torch.cuda.synchronize()
+    for n, v in want.items():
+        for a, b in zip(v if isinstance(v, tuple) else (v,), got[n] if isinstance(v, tuple) else (got[n],)):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), n
+
+
 def test_rows_past_32_bits(dev):
     """Element offsets past 2^32 in every row-wise call, checked on the last rows."""
     T, k, d = 75000, 8, 7168                                 # 4.3e9 elements in the sorted rows
