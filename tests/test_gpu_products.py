@@ -289,6 +289,15 @@ def test_every_fp32_tile_exact(dev, counts, N, K, out):
     run_all(counts, 3, N, K, F32, out, dev, seed=18)
 
 
+@pytest.mark.parametrize("N,K", [(136, 1 << 20), (1 << 20, 72)])
+@pytest.mark.parametrize("counts,dtype", [([40, 3], BF), ([300, 0], BF), ([40, 3], F32)], ids=["few-bf16", "bf16", "f32"])
+def test_widest_matrices_exact(dev, N, K, counts, dtype):
+    """The largest width: the longest sums (of -1, 0 and 1, exact in fp32), the farthest offsets within a tile."""
+    make = lambda shape, seed, dev: torch.randint(-1, 2, shape, device=dev, dtype=torch.int8,  # noqa: E731
+                                                  generator=torch.Generator(device=dev).manual_seed(seed)).float()
+    run_all(counts, 1, N, K, dtype, F32, dev, seed=19, make=make)
+
+
 def test_large_tiles_of_normal_values(dev):
     run_all([1500, 0, 17, 2579], 3, 2056, 520, BF, BF, dev, seed=13, make=normal, exact=False)
     run_all([1300, 900, 0, 1900], 0, 520, 2056, BF, F32, dev, seed=14, make=normal, exact=False)
