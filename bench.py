@@ -26,6 +26,7 @@ import argparse
 import hashlib
 import json
 import os
+import re
 import sys
 import time
 
@@ -36,16 +37,33 @@ METRIC = "MoE-layer tokens/s at 1 GPU; % MFMA peak (GEMM) and % HBM BW (permute/
 HBM_PEAK_GBPS = 8000.0            # MI355X HBM3E
 MFMA_PEAK_TFLOPS = {"bf16": 2500.0, "fp32": 157.3}
 COPY_CAL_BYTES = 1 << 30          # --calibrate-copy moves exactly this many bytes each way
-FFN_SOURCE = os.path.join(ROOT, "token_dispatch_expert_amd", "csrc", "ffn.hip")
+CSRC = os.path.join(ROOT, "token_dispatch_expert_amd", "csrc")
 
 
 def log(msg: str) -> None:
     print(f"[bench] {msg}", file=sys.stderr, flush=True)
 
 
-def source_sha(path: str) -> str:
-    with open(path, "rb") as f:
-        return hashlib.sha256(f.read()).hexdigest()[:16]
+def ffn_sources() -> list:
+    """The files of csrc that the grouped FFN's kernels are compiled from: ffn.hip and every header
+    there that it includes, directly or through another."""
+    found = ["ffn.hip"]
+    for name in found:  # (grows while it is walked)
+        with open(os.path.join(CSRC, name)) as f:
+            for header in re.findall(r'^\s*#\s*include\s+"([^"]+)"', f.read(), re.M):
+                if header not in found and os.path.exists(os.path.join(CSRC, header)):
+                    found.append(header)
+    return sorted(found)
+
+
+def source_sha(names: list) -> str:
+    """One digest over files of csrc, their names included."""
+    h = hashlib.sha256()
+    for name in names:
+        with open(os.path.join(CSRC, name), "rb") as f:
+            body = f.read()
+        h.update(f"{name} {len(body)}\n".encode() + body)
+    return h.hexdigest()[:16]
 
 
 def counter_traffic(workload: str):
@@ -55,7 +73,7 @@ def counter_traffic(workload: str):
         return None
     with open(p) as f:
         c = json.load(f)
-    if c.get("ffn_source_sha") != source_sha(FFN_SOURCE):
+    if c.get("ffn_source_sha") != source_sha(ffn_sources()):
         return None
     return c.get("hbm_bytes_per_call")
 
