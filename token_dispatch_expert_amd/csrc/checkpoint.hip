@@ -9,7 +9,7 @@
 // (1.0 GB, 5.8 TB/s; a fill reaches 6.8); 65,536 rows of 2048 go through moe_swiglu in 162 us
 // (6.7 TB/s) and its gradient in 216 - 229 us (1.35 GB, 5.9 - 6.2 TB/s).
 //
-// With s = 1 / (1 + e^-g) (fp32; e^-g overflowing gives s = 0, the limit):
+// With s = 1 / (1 + e^-g), in fp32, and in 64 bits where s is no normal fp32 number (far_sigmoid):
 //   h  = g s u
 //   du = dh g s
 //   dg = dh u s (1 + g (1 - s))
@@ -80,13 +80,32 @@ struct SwigluArgs {
   int E, rows, f;
 };
 
-// 1 / (1 + e^-g). For bf16 results the hardware's exp2 and reciprocal (each within one unit of
-// fp32, and the product with log2 e within |g| 2^-24) are far inside the result's rounding;
-// e^-g past the range gives 0, the limit.
+// 1 / (1 + e^-g) for g >= kFar. For bf16 results the hardware's exp2 and reciprocal (each within
+// one unit of fp32, and the product with log2 e within |g| 2^-24) are far inside the result's
+// rounding.
 template <typename T>
 __device__ __forceinline__ float sigmoid(float g) {
   if constexpr (sizeof(T) == 2) return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504088896f));
   else return 1.0f / (1.0f + expf(-g));
+}
+
+// Below kFar s = e^g leaves the normal fp32 numbers (2^-126 at g = -87.3): the reciprocal would flush
+// it to 0 and, from -88.7 on, e^-g would overflow, however large the factors that s meets. There the
+// products are taken in 64 bits and rounded to fp32 once, with s = (e^(g/4))^4: a quarter's power
+// is a normal fp32 number down to g = -349, where s is under 2^-503 and every product with fp32
+// factors is 0. One comparison per 8 elements where no g is that low.
+constexpr float kFar = -87.0f;
+__device__ __forceinline__ bool any_far(const F8& g) {
+  float low = g.v[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) low = fminf(low, g.v[i]);  // (NaN is passed over: it needs no care)
+  return low < kFar;
+}
+template <typename T>
+__device__ __forceinline__ double far_sigmoid(float g) {
+  // bf16: the hardware's exp2 and the product with log2 e leave s within 2^-15 of itself, inside the rounding
+  const double q = sizeof(T) == 2 ? __builtin_amdgcn_exp2f(g * (0.25f * 1.44269504088896f)) : expf(0.25f * g);
+  return (q * q) * (q * q);
 }
 
 template <typename T>
@@ -116,6 +135,11 @@ __global__ __launch_bounds__(kRowThreads) void swiglu_kernel(RowMap m, SwigluArg
   F8 h;
 #pragma unroll
   for (int i = 0; i < 8; ++i) h.v[i] = g.v[i] * sigmoid<T>(g.v[i]) * u.v[i];
+  if (any_far(g)) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (g.v[i] < kFar) h.v[i] = (float)(g.v[i] * far_sigmoid<T>(g.v[i]) * u.v[i]);
+  }
   store8_once(static_cast<T*>(p.h) + at, h);
 }
 
@@ -144,6 +168,16 @@ __global__ __launch_bounds__(kRowThreads) void swiglu_backward_kernel(RowMap m, 
     h.v[i] = silu * u.v[i];
     du.v[i] = dh.v[i] * silu;
     dg.v[i] = dh.v[i] * u.v[i] * s * (1.0f + g.v[i] * (1.0f - s));
+  }
+  if (any_far(g)) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (g.v[i] < kFar) {  // 1 - s is 1
+        const double s = far_sigmoid<T>(g.v[i]), silu = g.v[i] * s;
+        h.v[i] = (float)(silu * u.v[i]);
+        du.v[i] = (float)(silu * dh.v[i]);
+        dg.v[i] = (float)((double)dh.v[i] * u.v[i] * s * (1.0 + g.v[i]));
+      }
   }
   store8_once(static_cast<T*>(p.dg) + at, dg);
   store8_once(static_cast<T*>(p.du) + at, du);
