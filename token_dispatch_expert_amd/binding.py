@@ -476,8 +476,8 @@ def moe_checkpoint_unpack(codes, scales, out, flat_to_sorted=None, stream=None):
     rows = T if flat_to_sorted is None else flat_to_sorted.numel()
     if flat_to_sorted is not None:
         _need(flat_to_sorted, torch.int32, (rows,), "flat_to_sorted")
-    if T and rows % T:
-        raise ValueError("flat_to_sorted must have k entries for every row")
+        if (rows % T or rows < T) if T else rows:  # (k >= 1; no entries without tokens)
+            raise ValueError("flat_to_sorted must have k entries for every row")
     _need(out, out.dtype, (rows, d), "out")
     _call("moe_checkpoint_unpack", stream, codes, scales, T, rows // T if T else 1, d,
           flat_to_sorted, out, _float_dt(out, "out"))
