@@ -423,8 +423,8 @@ moe_status_t moe_swiglu(const void* g, const void* u, moe_dtype_t dtype, const i
 /*
  * moe_swiglu_backward - with s = 1 / (1 + e^-g):
  *     du = dh g s,   dg = dh u s (1 + g (1 - s)),   h = g s u
- *   computed in fp32, and in 64 bits where g < -87 and s is no normal fp32 number (as in
- *   moe_swiglu), so that a large factor beside a small s gives what it should.
+ *   computed in fp32, in this order of factors, and where g < -87, as in moe_swiglu, in 64 bits
+ *   (s is no normal fp32 number there).
  *   dh       [rows, d_ff] in dtype (MOE_BF16 or MOE_F32); dg, du out and h out (or NULL), same
  *            shape and dtype. h is the forward result again, for the down projection's weight
  *            gradient.

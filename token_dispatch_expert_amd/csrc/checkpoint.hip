@@ -93,7 +93,9 @@ __device__ __forceinline__ float sigmoid(float g) {
 // it to 0 and, from -88.7 on, e^-g would overflow, however large the factors that s meets. There the
 // products are taken in 64 bits and rounded to fp32 once, with s = (e^(g/4))^4: a quarter's power
 // is a normal fp32 number down to g = -349, where s is under 2^-503 and every product with fp32
-// factors is 0. One comparison per 8 elements where no g is that low.
+// factors is 0. One comparison per 8 elements where no g is that low; these results are stored over
+// the ordinary ones, which need not wait for them then (65,536 rows of 2048 forward and back: 387.2 us
+// without this, 388.0 with it, 389.4 where one store comes after the branch).
 constexpr float kFar = -87.0f;
 __device__ __forceinline__ bool any_far(const F8& g) {
   float low = g.v[0];
@@ -135,12 +137,13 @@ __global__ __launch_bounds__(kRowThreads) void swiglu_kernel(RowMap m, SwigluArg
   F8 h;
 #pragma unroll
   for (int i = 0; i < 8; ++i) h.v[i] = g.v[i] * sigmoid<T>(g.v[i]) * u.v[i];
+  store8_once(static_cast<T*>(p.h) + at, h);
   if (any_far(g)) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (g.v[i] < kFar) h.v[i] = (float)(g.v[i] * far_sigmoid<T>(g.v[i]) * u.v[i]);
+    store8_once(static_cast<T*>(p.h) + at, h);
   }
-  store8_once(static_cast<T*>(p.h) + at, h);
 }
 
 template <typename T, bool HELD>
@@ -169,6 +172,9 @@ __global__ __launch_bounds__(kRowThreads) void swiglu_backward_kernel(RowMap m, 
     du.v[i] = dh.v[i] * silu;
     dg.v[i] = dh.v[i] * u.v[i] * s * (1.0f + g.v[i] * (1.0f - s));
   }
+  store8_once(static_cast<T*>(p.dg) + at, dg);
+  store8_once(static_cast<T*>(p.du) + at, du);
+  if (p.h) store8_once(static_cast<T*>(p.h) + at, h);
   if (any_far(g)) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -178,10 +184,10 @@ __global__ __launch_bounds__(kRowThreads) void swiglu_backward_kernel(RowMap m, 
         du.v[i] = (float)(silu * dh.v[i]);
         dg.v[i] = (float)((double)dh.v[i] * u.v[i] * s * (1.0 + g.v[i]));
       }
+    store8_once(static_cast<T*>(p.dg) + at, dg);
+    store8_once(static_cast<T*>(p.du) + at, du);
+    if (p.h) store8_once(static_cast<T*>(p.h) + at, h);
   }
-  store8_once(static_cast<T*>(p.dg) + at, dg);
-  store8_once(static_cast<T*>(p.du) + at, du);
-  if (p.h) store8_once(static_cast<T*>(p.h) + at, h);
 }
 
 }  // namespace
