@@ -7,9 +7,11 @@
 // p(t, j) = flat_to_sorted[t*k + j]; an entry that names no row (an assignment dropped for its
 // expert's capacity) has no gradient. Sums are fp32 in a fixed order, without atomics.
 //
-// All three are bound by HBM. 8,192 tokens, 8 experts each, d = 7168, bf16 gradients: combine 540 us
-// (2.9 GB: y_sorted once, dy once per token, dy_sorted written; 5.4 TB/s, where a copy of 2 GiB
-// reaches 4.8), permute 168 us (1.06 GB, 6.3 TB/s), route 8 us for 256 experts.
+// Combine and permute are bound by HBM. 8,192 tokens, 8 experts each, d = 7168, bf16 gradients: combine
+// 540 - 568 us (2.9 GB: y_sorted once, dy once per token, dy_sorted written; 5.2 - 5.4 TB/s, where a copy of
+// 2 GiB reaches 4.8), permute 168 - 176 us (1.06 GB, 6.0 - 6.3 TB/s). Route, 256 experts, 7.1 us for 8.4 MB:
+// an almost empty launch of it takes 2.6 - 2.9 us, then a wave's 4 stores of 256 bytes follow a loop over
+// the k slots each.
 #include "rows.h"
 
 namespace moe {
@@ -130,8 +132,10 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const float* __rest
   }
 }
 
-// Workgroups of combine_backward_kernel: a row takes a whole workgroup from 1024 elements on
-// (two units of 8 per thread and less leave waves idle below), else a wave.
+// Workgroups of combine_backward_kernel: a row of more than 1024 elements takes a whole workgroup, else a
+// wave. Four waves to a row against one, 8,192 tokens: d = 1024 100 and 80 us, 1544 146 and 127 (a
+// workgroup takes 2048 elements at a time, so that waves idle up to there), 2048 176 and 173, 4096 325 and
+// 334; 64 tokens: 1544 4.4 and 4.3, 4096 4.3 and 5.7.
 constexpr int kWideRow = 1024;
 
 template <typename TI, typename TO>
@@ -140,8 +144,8 @@ hipError_t launch_combine_backward_t(const void* dy, const float* ys, const int3
   const unsigned grid = (unsigned)combine_backward_grid(T, k, d);
   const TI* s = static_cast<const TI*>(dy);
   TO* o = static_cast<TO*>(dys);
-  // Rows that do not fit the last-level cache are stored non-temporally: 940 MB of them 540 us against
-  // 570; 235 MB, which the next product finds there, 138 against 133.
+  // Rows that do not fit the last-level cache are stored non-temporally: 940 MB of them 568 us against
+  // 601; 235 MB, which the next product finds there, 145 against 138.
   const bool past_cache = (long long)T * k * d * (long long)sizeof(TO) > kCacheBytes;
   auto kern = d > kWideRow ? (past_cache ? &combine_backward_kernel<TI, TO, 4, true> : &combine_backward_kernel<TI, TO, 4, false>)
                            : (past_cache ? &combine_backward_kernel<TI, TO, 1, true> : &combine_backward_kernel<TI, TO, 1, false>);

@@ -5,9 +5,9 @@
 // (hold8 in rows.h): a value is code * scale, with a relative error of at most 2^-4 above the
 // code's subnormal range, and exact in bf16, so nothing is rounded a second time on the way
 // back. Every kernel here is bound by HBM: one pass, 16 bytes a thread and operand. 8,192 rows of 7168
-// (bf16) are packed in 28 us (6.3 TB/s) and unpacked into their 65,536 sorted rows in 174 us
-// (1.0 GB, 5.8 TB/s; a fill reaches 6.8); 65,536 rows of 2048 go through moe_swiglu in 162 us
-// (6.7 TB/s) and its gradient in 216 - 229 us (1.35 GB, 5.9 - 6.2 TB/s).
+// (bf16) are packed in 28 us (6.3 TB/s) and unpacked into their 65,536 sorted rows in 174 - 183 us
+// (1.0 GB, 5.5 - 5.8 TB/s; a fill reaches 6.8); 65,536 rows of 2048 go through moe_swiglu in 161 us
+// (6.7 TB/s) and its gradient in 199 - 230 us (1.35 GB, 5.9 - 6.8 TB/s).
 //
 // With s = 1 / (1 + e^-g), in fp32, and in 64 bits where s is no normal fp32 number (far_sigmoid):
 //   h  = g s u
@@ -214,8 +214,8 @@ static hipError_t launch_unpack_t(const void* codes, const float* scales, int T_
                                   void* out, hipStream_t stream) {
   const RowMap m = row_map(d / 8);
   // Non-temporal stores pay where a store instruction writes whole lines and the rows do not fit the
-  // last-level cache: to 65,536 bf16 rows of 7168 177 us against 193, of 7176 263 against 233, to
-  // 16,384 of 7168 45 against 37. In fp32 an instruction writes half of each line: 850 us against 356.
+  // last-level cache: to 65,536 bf16 rows of 7168 183 us against 199, of 7176 270 against 247, to
+  // 16,384 of 7168 47 against 31. In fp32 an instruction writes half of each line: 874 us against 373.
   const bool past_cache = sizeof(T) == 2 && d % 64 == 0 && (long long)T_ * k * d * 2 > kCacheBytes;
   auto kern = m.shift < 6 ? &unpack_kernel<T, false, false>
                           : (past_cache ? &unpack_kernel<T, true, true> : &unpack_kernel<T, true, false>);

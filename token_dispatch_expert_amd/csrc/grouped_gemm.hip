@@ -32,9 +32,9 @@ namespace {
 // lane (row or column lane % 16, element lane / 16); lane group g takes elements 4g .. 4g + 3
 // of a 16-long slice in turn, the same for both operands, so an along fragment is one 16-byte
 // read. The operands go in as (B, A), which gives each lane 4 consecutive columns of one row of C.
-// Bound by the matrix instructions: 16,384 rows over 8 experts of 1024 x 2048 take 547 us forward
-// (126 TFLOP/s; a large fp32 library product reaches 132), 1.09 ms for two input gradients, 542 us
-// for the weight gradient. Tiles of 128 measured slower at every size, by 9 to 19%. With few tiles it
+// Bound by the matrix instructions: 16,384 rows over 8 experts of 1024 x 2048 take 548 - 558 us
+// forward (123 - 125 TFLOP/s; a large fp32 library product reaches 132), 1.09 - 1.11 ms for two input
+// gradients, 554 us for the weight gradient. Tiles of 128 measured slower at every size, by 9 to 19%. With few tiles it
 // is the chain of a step that bounds (LDS, barriers, dependent products); two to four steps' loads
 // ahead gained nothing there.
 constexpr int kStep = 32;
@@ -97,8 +97,12 @@ struct OutTile {
 // consecutive columns (from 4 (lane / 16)) of row lane % 16 in each 16-column fragment. Stored
 // like that, an instruction would write 64 bytes (fp32) or 32 (bf16) of each of 16 rows; lanes
 // first exchange parts so that it writes 128 bytes of each of 8 (2% of the large products' time),
-// most often non-temporally (stream_rows), which leaves the L2 to the operands (weight gradients of
-// 128 rows per expert: 526 against 424 us).
+// most often non-temporally (stream_rows), which leaves the L2 to the operands (fp32 weight gradients of 64
+// experts of 2048 x 4096, 128 rows each: 515 against 422 us). Tiles whose waves have too few columns for
+// the exchange (one fragment, or up to two with bf16 results: tiles for few rows) and results that are
+// added to what is there store fragment by fragment, plainly. For the latter HBM bounds that: the fp32 weight
+// gradient of 32 experts of 2048 x 7168 reads dw once more (1.9 GB by counter) and takes, for 65,536 rows, 2.17 ms
+// against 1.83, for 1,024 rows 0.88 (3.85 GB, 4.4 TB/s) against 0.35.
 template <int NF>
 __device__ __forceinline__ void store_fragments(const OutTile& o, const ProductArgs& p, const f32x4 (&v)[NF], int r0,
                                                 int c0, int lane) {
@@ -491,14 +495,16 @@ __device__ __forceinline__ void wait_steps(int n) {
 // a partial tile costs what its rows need; waves w and w + 4 share a SIMD and own different
 // halves of the tile, so every SIMD has work.
 //
-// Measured, 65,536 rows dealt by Zipf 1.2 to 32 experts of 2048 x 7168 (bf16): forward 1.60 ms
-// (1.20 PFLOP/s), two input gradients 3.11 ms (1.24), fp32 weight gradients 1.85 ms (1.04); a
-// library product of these sizes without the experts reaches 1.34, 1.13 and 1.02. The clock
-// falls to 1.9 - 2.05 GHz under the power limit; of the cycles the matrix instructions take 59%
+// Measured, 65,536 rows dealt by Zipf 1.2 to 32 experts of 2048 x 7168 (bf16): forward 1.56 - 1.62 ms
+// (1.19 - 1.23 PFLOP/s), two input gradients 3.09 - 3.23 ms (1.19 - 1.25), fp32 weight gradients 1.83 -
+// 1.91 ms (1.01 - 1.05); a library product of these sizes without the experts reaches 1.34, 1.13 and
+// 1.02. The sums over the contraction are one chain per value: 4.0e-7 from the 64-bit result on the decode
+// product below, where a library product in fp32 is 3.7e-7 from it; a second set of accumulators does not
+// fit beside the large tile's. The clock falls to 1.9 - 2.05 GHz under the power limit; of the cycles the matrix instructions take 59%
 // (forward, input gradients) and 47% (weight gradients, whose 1.9 GB of fp32 stores take another
 // 20%). LDS is busy 18 - 23% without bank conflicts; taking out, one by one, LDS reads, loads that
 // hit in the L2 and those that miss it gives back about 9% of the time each. Few rows are bound by the
-// stream of the weights: 1,024 rows over 128 experts of 1536 x 4096 take 245 us (1.6 GB, 6.5 TB/s),
+// stream of the weights: 1,024 rows over 128 experts of 1536 x 4096 take 252 us (1.6 GB, 6.4 TB/s),
 // 8 rows on 8 of them 18 us (101 MB, 5.6 TB/s).
 //
 // The tile: 256 x 256 with 8 waves of 128 x 64 has the most products per byte that the registers
@@ -540,7 +546,7 @@ __global__ __launch_bounds__(64 * WGM * WGN) void tile_kernel(ProductArgs p) {
   const ptrdiff_t moved_b = pair ? static_cast<const char*>(p.b2) - static_cast<const char*>(p.b) : 0;
   const int steps1 = (t.kdim + DK - 1) / DK, steps = pair ? 2 * steps1 : steps1;
   // The expert's weights are read by this row tile alone, in whole lines (1,024 rows on 128 experts of
-  // 1536 x K, two input gradients: K = 4096 436 us against 476 with plain loads, K = 4104 509 against 457).
+  // 1536 x K, two input gradients: Zipf 1.2: K = 4096 439 us against 484 with plain loads, K = 4104 517 against 470).
   const bool once = ONCE && t.rb - t.ra <= TM && p.K % 64 == 0;
 
   auto issue = [&](int st) __attribute__((always_inline)) {
@@ -662,7 +668,7 @@ double expected_tiles(GroupedProduct kind, const GroupedGemmArgs& a, int TM, int
 // Time, per contraction step of 64 (us), of TM x TN tiles over the CUs, `fit` to each at a time: `full`
 // where the CUs are filled, `alone` for a last round with at most one tile to a CU. The times are from
 // products of 512 to 8192 rows over 1 to 16 experts (forward, 1024 rows of 2048 x 7168 for one expert:
-// 136 us in tiles of 256, 78 of 128, 59 of 64 x 128; 4096 rows of 4096 x 1024 for 8 experts: 33, 43 and 55).
+// 138 us in tiles of 256, 83 of 128, 59 of 64 x 128; 4096 rows of 4096 x 1024 for 8 experts: 33, 44 and 56).
 struct TileCost {
   int TM, TN, fit;
   double alone, full;
@@ -678,9 +684,9 @@ double step_time(GroupedProduct kind, const GroupedGemmArgs& a, const TileCost& 
 // Whether C's rows are stored non-temporally. Rows of whole 128-byte lines always are. Others share lines
 // between tiles and between a row's pieces; those lines are put together in the L2 if they may stay
 // there, which pays unless the products are long enough that the L2 is worth more to the operands
-// (16,384 rows over 8 experts of 3288 x K, bf16, plain and non-temporal: K = 264 60 and 70 us, 1032 130
-// and 141, 4104 507 and 495; weight gradients of 42 experts of 2488 x 3288, bf16: 64 rows per expert 220 and
-// 287 us, 256 376 and 334; fp32: 256 rows 496 and 612, 512 690 and 670).
+// (16,384 rows over 8 experts of 3288 x K, bf16, plain and non-temporal: K = 264 55 and 67 us, 1032 127
+// and 137, 4104 508 and 493; weight gradients of 42 experts of 2488 x 3288, bf16: 64 rows per expert 213 and
+// 278 us, 256 357 and 309; fp32: 256 rows 480 and 592, 512 641 and 620).
 int stream_rows(const GroupedGemmArgs& a, GroupedProduct kind) {
   const long long cols = kind == kForward ? a.N : a.K;
   if (cols * (a.out_bf16 ? 2 : 4) % 128 == 0) return 1;
@@ -694,11 +700,11 @@ hipError_t launch_product(const GroupedGemmArgs& a, int cus, hipStream_t stream)
                       a.out_bf16 ? 1 : 0, a.accumulate ? 1 : 0, stream_rows(a, P)};
   if (!a.bf16) {
     // Few rows leave most of a 64-row tile's products empty: at 64 experts of 1024 x 2048, even rows,
-    // tiles of 16 x 64 against 64 x 64 took (forward) 124 and 166 us at 1 row per expert, 128 and
-    // 165 at 32, 235 and 180 at 64. The contraction is split over the waves where there are few tiles
-    // (one expert of 1024 x 1024, 512 rows, forward: 31 us in tiles of 64 x 64, 27 split in two, 22 in tiles of
-    // 16 x 64 split in four; 4 experts, 1,024 rows, input gradients 35, 28 and 39) or one row tile per
-    // expert (the 64 experts at 1 row 96 us against 124); at 32 rows each it costs (145 against 134).
+    // tiles of 16 x 64 against 64 x 64 took (forward) 123 and 148 us at 1 row per expert, 125 and
+    // 162 at 32, 205 and 170 at 64. The contraction is split over the waves where there are few tiles
+    // (one expert of 1024 x 1024, 512 rows, forward: 28 us in tiles of 64 x 64, 24 split in two, 20 in tiles of
+    // 16 x 64 split in four; 4 experts, 1,024 rows, input gradient 31, 26 and 36) or one row tile per
+    // expert (the 64 experts at 1 row 97 us against 123); at 32 rows each it costs (133 against 125).
     if constexpr (P == kWgrad) {
       // few tiles of many rows: one expert of 1024 x 1024, 4,096 rows 87 us against 113
       if (a.rows / a.E >= 128 && expected_tiles(P, a, 64, 64) <= cus) return launch_f32<P, 2, 2, 2, 2>(a, p, stream);
@@ -714,41 +720,41 @@ hipError_t launch_product(const GroupedGemmArgs& a, int cus, hipStream_t stream)
   // Which tiles, from the sizes alone (the host does not know the offsets). Measured at 64 experts of
   // 2048 x 4096, rows spread evenly (us):
   //   rows per expert             8     16     32     64     96    128    256    512
-  //   forward  32 x 64 tiles    163    178
-  //            64 x 128         184    187    192    204           273    448    833
-  //            128 x 128        237    239    239    249           262    362    650
-  //            256 x 256        247    243    245    254           268    298    491
-  //   dgrad 2  32 x 128         325    335
-  //            64 x 128         329    338    352    391           565    945   1804
-  //            128 x 128        362    365    372    394           433    714   1321
-  //            256 x 256        376    378    384    390           420    534    980
-  //   wgrad    128 x 128, fp32  334           354    365           424    605    961
-  //            256 x 256, fp32  420           433    437           474    557    781
-  //            128 x 128, bf16                237    249    305    316    573    859
-  //            256 x 256, bf16                233    239    273    284    412    725
-  // With rows dealt by Zipf 1.2 or 0.6 the borders are the same or a little lower, but forward tiles of
-  // 128 stay ahead to about 192 rows (128 per expert, Zipf 0.6: 257 us against 311). With 1 row per
-  // expert a bf16 weight gradient takes 186 us in tiles of 128, 204 in tiles of 256. Large tiles
-  // are wasted on a width that fills less than one of them, and where there are fewer of them than
-  // CUs (step_time).
+  //   forward  32 x 64 tiles    164    172    188    257    325    413    740   1368
+  //            64 x 128         181    184    190    198    249    265    439    822
+  //            128 x 128        220    222    225    227    230    234    351    634
+  //            256 x 256        241    242    245    250    255    259    281    479
+  //   dgrad 2  32 x 128         322    341    357    497    580    720   1295   2444
+  //            64 x 128         328    334    347    364    529    553    922   1747
+  //            128 x 128        328    335    340    359    383    396    704   1309
+  //            256 x 256        375    377    381    389    394    413    527    971
+  //   wgrad    128 x 128, fp32  341    352    360    368    415    422    584   1001
+  //            256 x 256, fp32  429    439    439    443    471    476    560    758
+  //            128 x 128, bf16  228    244    249    261    312    319    460    850
+  //            256 x 256, bf16  220    228    229    238    279    286    389    618
+  // (Where two are within 7% the rule may take either.) With rows dealt by Zipf 1.2 or 0.6 the borders are the
+  // same or a little lower, but forward tiles of 128 stay ahead at 128 rows (Zipf 0.6: 259 us against
+  // 326; at 192, evenly dealt, 325 against 271). With 1 row per expert a bf16 weight gradient takes 175 us
+  // in tiles of 128, 189 in tiles of 256 (Zipf 1.2; evenly dealt 226 and 220). Large tiles are wasted on
+  // a width that fills less than one of them, and where there are fewer of them than CUs (step_time).
   const long long mean = a.rows / a.E;
   const double big = step_time(P, a, kBig, cus), mid = step_time(P, a, kMid, cus);
   if constexpr (P == kWgrad) {
     if (mean >= (a.out_bf16 ? 16 : 160) && a.N > 128 && a.K > 128 && big <= mid)
       return launch_tiles<P, 128, 64, 2, 4, 64, 2, false, true>(a, p, stream);
     // With a CU to each tile, eight waves and steps of 128: one expert of 1024 x 1024, 8,192 rows 63 us
-    // against 91.
+    // against 96.
     if (expected_tiles(P, a, 128, 128) <= cus)
       return launch_tiles<P, 64, 32, 2, 4, 128, 2, false, false>(a, p, stream);
     return launch_tiles<P, 64, 64, 2, 2, 64, 2, false, false>(a, p, stream);
   } else {
     // With a CU to each tile, the smallest tiles of which that is so, with as many steps in flight as the
     // LDS holds, eight waves and steps of 128 (in steps of 64 their waits and barriers take most of the
-    // time). One expert of 1024 x 2048, forward: 256 rows 10.4 us in tiles of 32 x 64 against 18.7 in the
-    // three-slot tiles of 64 x 128; 1,024 rows 14.6 in these tiles of 64 x 128 against 18.7; 4,096 rows 23.5
-    // in these of 128 against 27.2 in the ones for full CUs. Input gradients of two with 1024 x 2048: 1,536
-    // rows 27.6 against 41.4, 4,096 rows 39.9 against 53.7. One token for 8 of 128 experts of 1536 x 4096
-    // 17.9 against 18.5.
+    // time). One expert of 1024 x 2048, forward: 256 rows 10.0 us in tiles of 32 x 64 against 17.5 in the
+    // three-slot tiles of 64 x 128; 1,024 rows 14.4 in these tiles of 64 x 128 against 18.5; 4,096 rows 23.0
+    // in these of 128 against 28.0 in the ones for full CUs. Input gradients of two: 1,536 rows 20.8 in these of
+    // 128 against 28.4; 512 rows over 8 such experts 19.0 in these of 64 x 128 against 22.7. One token for 8 of 128
+    // experts of 1536 x 4096 takes 18.5 in rings of six and of three.
     const auto few = [&](int TM, int TN) { return expected_tiles(P, a, TM, TN) <= cus; };
     if constexpr (P == kForward) {
       if (few(32, 64)) return launch_tiles<P, 32, 16, 1, 4, 128, 6, true, false>(a, p, stream);

@@ -35,8 +35,8 @@ inline long long row_grid(const RowMap& m, long long rows) {
   return (m.slices > 1 ? (groups + 7) / 8 * 8 : groups) * m.slices;
 }
 // WIDE: m.shift >= 6. The row is then the same for a whole workgroup, and the compiler knows it: summing
-// 8 rows of 14 KB for each of 8192 tokens took 227 us with the row's number (and so its map entries)
-// per lane, 168 us like this.
+// 8 rows of 14 KB for each of 8192 tokens took 231 us with the row's number (and so its map entries)
+// per lane, 176 us like this.
 template <bool WIDE = false>
 __device__ __forceinline__ void row_unit(const RowMap& m, unsigned& row, int& unit) {
   unsigned group = blockIdx.x, slice = 0;
@@ -54,7 +54,7 @@ struct F8 {
   float v[8];
 };
 // ..._once: non-temporal, for data that the kernel reads or writes once: its lines leave the caches
-// first. At 65,536 rows of 2048 the SwiGLU gradient took 235 us without and 214 us with them; loads of rows
+// first. At 65,536 rows of 2048 the SwiGLU gradient took 239 us without and 199 us with them; loads of rows
 // that several workgroups read stay plain, and stores where a kernel says why.
 __device__ __forceinline__ F8 load8_once(const float* p) {
   const f32x4 a = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p));
