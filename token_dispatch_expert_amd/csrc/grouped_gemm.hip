@@ -496,7 +496,7 @@ __device__ __forceinline__ void wait_steps(int n) {
 // halves of the tile, so every SIMD has work.
 //
 // Measured, 65,536 rows dealt by Zipf 1.2 to 32 experts of 2048 x 7168 (bf16): forward 1.56 - 1.62 ms
-// (1.19 - 1.23 PFLOP/s), two input gradients 3.09 - 3.23 ms (1.19 - 1.25), fp32 weight gradients 1.83 -
+// (1.19 - 1.23 PFLOP/s), two input gradients 3.09 - 3.26 ms (1.18 - 1.25), fp32 weight gradients 1.83 -
 // 1.91 ms (1.01 - 1.05); a library product of these sizes without the experts reaches 1.34, 1.13 and
 // 1.02. The sums over the contraction are one chain per value: 4.0e-7 from the 64-bit result on the decode
 // product below, where a library product in fp32 is 3.7e-7 from it; a second set of accumulators does not
