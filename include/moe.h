@@ -75,7 +75,8 @@ typedef enum {
   MOE_BF16 = 1,
   MOE_FP8_E4M3FN = 2,
   MOE_BF16_BLOCKED = 3,       /* weights only */
-  MOE_FP8_E4M3FN_BLOCKED = 4  /* weights only */
+  MOE_FP8_E4M3FN_BLOCKED = 4, /* weights only */
+  MOE_MXFP4 = 16              /* 4-bit codes with shared scales: the calls that name it */
 } moe_dtype_t;
 
 #define MOE_MAX_EXPERTS 1024
@@ -471,6 +472,44 @@ moe_status_t moe_permute_backward(const void* dx_sorted, moe_dtype_t dtype,
 moe_status_t moe_route_backward(const float* dgates, const int32_t* topk_ids,
                                 const float* topk_gates, int T, int E, int k, float* dlogits,
                                 void* stream);
+
+/*
+ * ---------------------------------------------------------------------------------------
+ * MXFP4: rows and weights in 4 bits
+ * ---------------------------------------------------------------------------------------
+ * The OCP microscaling format with e2m1 elements (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives) and one
+ * e8m0 scale byte b per 32 consecutive elements of a row, the contraction axis of a product; a value is
+ * code * 2^(b - 127), NaN for b = 255. A matrix of `rows` rows of d elements (d a multiple of 32) is
+ *   codes   [rows, d/2] bytes, row-major, element 2i in the low half of byte i;
+ *   scales  [ceil(d/256), rows, 8] bytes: the scale of row r, elements 32 g .. 32 g + 31, at
+ *           ((g / 8) * rows + r) * 8 + g % 8. (Scales stored [rows, d/32] elsewhere are brought into this order once.)
+ *           Bytes of groups past d are never used; the library writes 127 there.
+ * E matrices (weights [E, N, K]) lie one after the other, codes [E, N, K/2] and scales
+ * [E, ceil(K/256), N, 8]. The values that the kernels work with are exact in fp32 for every byte, and in bf16 too.
+ * Element counts may pass 2^32; a size whose kernels would need more than 2^32 threads gives MOE_ERR_UNSUPPORTED.
+ */
+
+/*
+ * moe_mxfp4_quantize - weights or rows to MXFP4.
+ *   x       [E, rows, d] in x_dtype (MOE_BF16 or MOE_F32).
+ *   flat_to_sorted  NULL (then k must be 1): codes and scales of E matrices of `rows` rows. Or [rows, k] int32
+ *           (then E must be 1), as moe_permute writes it: one matrix of rows * k rows, row t of x in each of its rows
+ *           flat_to_sorted[t*k + j]; entries outside [0, rows * k) are skipped (dropped assignments), and
+ *           rows that no entry names are left as they were.
+ *   The scale is the smallest power of two with which the group's largest magnitude is at most 6, between 2^-125
+ *   and 2^125 (1 for a group of zeros); codes are rounded once, to nearest even. (At scale 2^125 codes stop at 6.)
+ *   A group that holds a NaN or an infinity gets the scale 255 and codes 0: all of it is NaN.
+ */
+moe_status_t moe_mxfp4_quantize(const void* x, moe_dtype_t x_dtype, int E, int rows, int k, int d,
+                                const int32_t* flat_to_sorted, void* codes, void* scales,
+                                void* stream);
+
+/*
+ * moe_mxfp4_dequantize - the values of E matrices of `rows` rows, out [E, rows, d] in out_dtype (MOE_BF16
+ * or MOE_F32). Exact, but for values past 2^128, which are infinite.
+ */
+moe_status_t moe_mxfp4_dequantize(const void* codes, const void* scales, int E, int rows, int d,
+                                  void* out, moe_dtype_t out_dtype, void* stream);
 
 #ifdef __cplusplus
 }

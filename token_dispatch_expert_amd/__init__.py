@@ -10,5 +10,6 @@ from .binding import (  # noqa: F401
     moe_route, moe_expert_capacity, moe_route_gemm, moe_route_gemm_workspace_size,
     moe_block_weights, moe_checkpoint_pack, moe_checkpoint_unpack, moe_combine_backward,
     moe_grouped_gemm, moe_grouped_gemm_dgrad, moe_grouped_gemm_wgrad, moe_permute_backward,
-    moe_route_backward, moe_swiglu, moe_swiglu_backward,
+    moe_route_backward, moe_swiglu, moe_swiglu_backward, moe_mxfp4_quantize,
+    moe_mxfp4_dequantize, mxfp4_buffers,
 )

@@ -19,6 +19,7 @@ LIB_NAME = "libmoe.so"
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_HIP = range(5)
 MOE_F32, MOE_BF16, MOE_FP8_E4M3FN, MOE_BF16_BLOCKED, MOE_FP8_E4M3FN_BLOCKED = 0, 1, 2, 3, 4
+MOE_MXFP4 = 16
 
 _DTYPE_ENUM = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16,
                torch.float8_e4m3fn: MOE_FP8_E4M3FN, torch.uint8: MOE_FP8_E4M3FN}
@@ -31,7 +32,7 @@ ENTRY_POINTS = (
     "moe_block_weights",
     "moe_grouped_gemm", "moe_grouped_gemm_dgrad", "moe_grouped_gemm_wgrad", "moe_checkpoint_pack",
     "moe_checkpoint_unpack", "moe_swiglu", "moe_swiglu_backward", "moe_combine_backward",
-    "moe_permute_backward", "moe_route_backward",
+    "moe_permute_backward", "moe_route_backward", "moe_mxfp4_quantize", "moe_mxfp4_dequantize",
 )
 
 _lib = None
@@ -86,6 +87,8 @@ def load_library(path: str | None = None):
         "moe_combine_backward": ([P, I, P, P, P, I, I, I, P, I, P, P], I),
         "moe_permute_backward": ([P, I, P, I, I, I, P, I, P], I),
         "moe_route_backward": ([P, P, P, I, I, I, P, P], I),
+        "moe_mxfp4_quantize": ([P, I, I, I, I, I, P, P, P, P], I),
+        "moe_mxfp4_dequantize": ([P, P, I, I, I, P, I, P], I),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -568,6 +571,61 @@ def moe_route_backward(dgates, topk_ids, topk_gates, dlogits, stream=None):
     _need(topk_gates, torch.float32, (T, k), "topk_gates")
     _need(dlogits, torch.float32, (T, E), "dlogits")
     _call("moe_route_backward", stream, dgates, topk_ids, topk_gates, T, E, k, dlogits)
+
+
+# ----------------------------------------------------------------------------------------
+# MXFP4: rows and weights in 4 bits (same names as the C ABI)
+# ----------------------------------------------------------------------------------------
+_MX_CODE_DT = (torch.uint8, torch.float4_e2m1fn_x2)
+_MX_SCALE_DT = (torch.uint8, torch.float8_e8m0fnu)
+
+
+def mxfp4_buffers(shape, device="cuda"):
+    """Allocate (with torch) the codes and scales of rows (rows, d) or of weights (E, N, K)."""
+    *lead, rows, d = shape
+    return (torch.empty((*lead, rows, d // 2), dtype=torch.uint8, device=device),
+            torch.empty((*lead, -(-d // 256), rows, 8), dtype=torch.uint8, device=device))
+
+
+def _mx(codes, scales, shape, name):
+    """codes (uint8 or float4_e2m1fn_x2, two elements each) and scales (uint8 or float8_e8m0fnu) of a matrix of
+    MXFP4 rows, or of one for each expert."""
+    *lead, rows, d = shape
+    if codes.dtype not in _MX_CODE_DT:
+        raise TypeError(f"{name}: expected uint8 or float4_e2m1fn_x2, got {codes.dtype}")
+    if scales.dtype not in _MX_SCALE_DT:
+        raise TypeError(f"{name} scales: expected uint8 or float8_e8m0fnu, got {scales.dtype}")
+    _need(codes, codes.dtype, (*lead, rows, d // 2), name)
+    _need(scales, scales.dtype, (*lead, -(-d // 256), rows, 8), name + " scales")
+
+
+def moe_mxfp4_quantize(x, codes, scales, flat_to_sorted=None, stream=None):
+    """x [rows, d] or [E, N, K] (bfloat16 or float32) to MXFP4: codes [.., d/2] (uint8 or float4_e2m1fn_x2) and
+    scales [.., ceil(d/256), rows, 8] (uint8 or float8_e8m0fnu). With flat_to_sorted [rows*k], x [rows, d]: row
+    t goes to each of its k rows of codes [rows*k, d/2]."""
+    shape = x.shape
+    if len(shape) not in (2, 3):
+        raise ValueError(f"x: expected 2 or 3 dimensions, got shape {tuple(shape)}")
+    E, (rows, d) = shape[0] if len(shape) == 3 else 1, shape[-2:]
+    k = 1
+    if flat_to_sorted is not None:
+        R = flat_to_sorted.numel()
+        _need(flat_to_sorted, torch.int32, (R,), "flat_to_sorted")
+        if len(shape) != 2 or ((R % rows or R < rows) if rows else R):  # (k >= 1; no entries without rows)
+            raise ValueError("flat_to_sorted must have k entries for every row of x [rows, d]")
+        k, shape = R // rows if rows else 1, (R, d)
+    _mx(codes, scales, shape, "codes")
+    _call("moe_mxfp4_quantize", stream, x, _float_dt(x, "x"), E, rows, k, d, flat_to_sorted, codes, scales)
+
+
+def moe_mxfp4_dequantize(codes, scales, out, stream=None):
+    """The values of MXFP4 rows: out [rows, d] or [E, N, K] (bfloat16 or float32)."""
+    shape = out.shape
+    if len(shape) not in (2, 3):
+        raise ValueError(f"out: expected 2 or 3 dimensions, got shape {tuple(shape)}")
+    _mx(codes, scales, shape, "codes")
+    _call("moe_mxfp4_dequantize", stream, codes, scales, shape[0] if len(shape) == 3 else 1, *shape[-2:], out,
+          _float_dt(out, "out"))
 
 
 def layer_buffers(T: int, E: int, k: int, d: int, act_dtype, device="cuda",

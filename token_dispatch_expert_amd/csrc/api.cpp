@@ -9,6 +9,7 @@
 #include <vector>
 
 #include "moe_internal.h"
+#include "mxfp4_internal.h"
 
 namespace moe {
 
@@ -184,10 +185,11 @@ moe_status_t check_combine(const float* y_sorted, const int32_t* f2s, const floa
 
 // ---- training ----
 bool float_dtype(moe_dtype_t t) { return t == MOE_F32 || t == MOE_BF16; }
+bool known_dtype(moe_dtype_t t) { return (t >= MOE_F32 && t <= MOE_FP8_E4M3FN_BLOCKED) || t == MOE_MXFP4; }
 // MOE_OK for the two formats of activations and gradients, else why not
 moe_status_t check_float_dtype(moe_dtype_t t) {
   if (float_dtype(t)) return MOE_OK;
-  return t >= MOE_FP8_E4M3FN && t <= MOE_FP8_E4M3FN_BLOCKED ? MOE_ERR_UNSUPPORTED : MOE_ERR_INVALID_ARG;
+  return known_dtype(t) ? MOE_ERR_UNSUPPORTED : MOE_ERR_INVALID_ARG;
 }
 moe_status_t check_width(int d) {
   if (d < 1 || d > kMaxDim) return MOE_ERR_INVALID_ARG;
@@ -210,7 +212,7 @@ moe_status_t check_product(moe_dtype_t dtype, moe_dtype_t w_dtype, moe_dtype_t o
   if (s == MOE_OK) s = check_float_dtype(dtype);
   if (s == MOE_OK) s = check_float_dtype(out_dtype);
   if (s == MOE_OK && w_dtype != dtype)
-    s = w_dtype < MOE_F32 || w_dtype > MOE_FP8_E4M3FN_BLOCKED ? MOE_ERR_INVALID_ARG : MOE_ERR_UNSUPPORTED;
+    s = known_dtype(w_dtype) ? MOE_ERR_UNSUPPORTED : MOE_ERR_INVALID_ARG;
   if (s != MOE_OK) return s;
   if (a.E > MOE_MAX_EXPERTS) return MOE_ERR_UNSUPPORTED;
   const long long R = a.rows, W = (long long)a.E * a.N * a.K;
@@ -230,6 +232,14 @@ moe_status_t check_tokens(int T, int k, int d, const int32_t* f2s) {
   if (s != MOE_OK) return s;
   return ok_ptr(f2s, (long long)T * k, 4) ? MOE_OK : MOE_ERR_INVALID_ARG;
 }
+
+// ---- MXFP4 ----
+// A contraction or row length in groups of 32.
+moe_status_t check_mx_width(int d) {
+  if (d < 1 || d > kMaxDim) return MOE_ERR_INVALID_ARG;
+  return d % 32 == 0 ? MOE_OK : MOE_ERR_UNSUPPORTED;
+}
+long long mx_scale_bytes(long long rows, int d) { return (d + 255) / 256 * rows * 8; }
 
 moe_status_t hip_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
 
@@ -601,6 +611,39 @@ moe_status_t moe_route_backward(const float* dgates, const int32_t* topk_ids,
   if ((T + 3LL) / 4 > moe::kMaxWorkgroups) return MOE_ERR_UNSUPPORTED;
   return hip_status(moe::launch_route_backward(dgates, topk_ids, topk_gates, T, E, k, dlogits,
                                                static_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_mxfp4_quantize(const void* x, moe_dtype_t x_dtype, int E, int rows, int k, int d,
+                                const int32_t* flat_to_sorted, void* codes, void* scales,
+                                void* stream) {
+  if (E < 1 || rows < 0 || k < 1 || k > MOE_MAX_TOPK) return MOE_ERR_INVALID_ARG;
+  if (flat_to_sorted ? E != 1 : k != 1) return MOE_ERR_INVALID_ARG;
+  moe_status_t s = check_mx_width(d);
+  if (s == MOE_OK) s = check_float_dtype(x_dtype);
+  if (s != MOE_OK) return s;
+  const long long n = (long long)E * rows, to = n * k;
+  if (to > INT_MAX) return MOE_ERR_INVALID_ARG;
+  if (!ok_ptr(x, n * d, 16) || !ok_ptr(codes, to * d, 16) || !ok_ptr(scales, mx_scale_bytes(to, d), 16) ||
+      !aligned(flat_to_sorted, 4))
+    return MOE_ERR_INVALID_ARG;
+  if (moe::mx_row_grid(n, d) > moe::kMaxWorkgroups) return MOE_ERR_UNSUPPORTED;
+  return hip_status(moe::launch_mx_quantize(x, x_dtype == MOE_BF16, E, rows, k, d, flat_to_sorted, codes, scales,
+                                            static_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_mxfp4_dequantize(const void* codes, const void* scales, int E, int rows, int d,
+                                  void* out, moe_dtype_t out_dtype, void* stream) {
+  if (E < 1 || rows < 0) return MOE_ERR_INVALID_ARG;
+  moe_status_t s = check_mx_width(d);
+  if (s == MOE_OK) s = check_float_dtype(out_dtype);
+  if (s != MOE_OK) return s;
+  const long long n = (long long)E * rows;
+  if (n > INT_MAX) return MOE_ERR_INVALID_ARG;
+  if (!ok_ptr(codes, n * d, 16) || !ok_ptr(scales, mx_scale_bytes(n, d), 16) || !ok_ptr(out, n * d, 16))
+    return MOE_ERR_INVALID_ARG;
+  if (moe::mx_row_grid(n, d) > moe::kMaxWorkgroups) return MOE_ERR_UNSUPPORTED;
+  return hip_status(moe::launch_mx_dequantize(codes, scales, E, rows, d, out, out_dtype == MOE_BF16,
+                                              static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"
