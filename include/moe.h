@@ -245,21 +245,22 @@ moe_status_t moe_block_weights(const void* src, void* dst, moe_dtype_t w_dtype, 
  *             Wg, Wu [d, d_ff] and Wd [d_ff, d]).
  *   w_dtype   MOE_F32 with act MOE_F32; MOE_BF16, MOE_FP8_E4M3FN, MOE_BF16_BLOCKED (each of the
  *             E matrices of w_gate, w_up, w_down in the blocked layout above; d and d_ff
- *             multiples of 64) or MOE_FP8_E4M3FN_BLOCKED (d and d_ff at most 65536) with act
- *             MOE_BF16.
+ *             multiples of 64), MOE_FP8_E4M3FN_BLOCKED (d and d_ff at most 65536) or MOE_MXFP4
+ *             (codes; see the section on MXFP4) with act MOE_BF16.
  *   s_gate, s_up [E, ceil(d_ff/128), ceil(d/128)], s_down [E, ceil(d/128), ceil(d_ff/128)]
  *             fp32 per-128x128-block scales of the stored matrices (fp8 only, else NULL):
- *             the weight value is code * scale of its block.
+ *             the weight value is code * scale of its block. MOE_MXFP4: the scale bytes, 16-byte
+ *             aligned, [E, ceil(d/256), d_ff, 8] and [E, ceil(d_ff/256), d, 8].
  *   y_sorted  [rows, d] fp32 out.
  *   Arithmetic: fp32 accumulation; with act MOE_BF16, h is rounded to bf16 (RNE) between
  *   the two GEMMs; fp8 codes are converted exactly and the block scale multiplies the fp32
  *   partial sum of each 128-long contraction block.
- *   Requires d and d_ff multiples of 8 (of 128 for fp8). Experts with no rows are never read.
+ *   Requires d and d_ff multiples of 8 (of 128 for fp8, of 32 for MXFP4). Experts with no rows are never read.
  */
 moe_status_t moe_grouped_ffn(const void* x_sorted, moe_dtype_t act_dtype, const int32_t* offsets,
                              int rows, int E, int d, int d_ff, const void* w_gate,
                              const void* w_up, const void* w_down, moe_dtype_t w_dtype,
-                             const float* s_gate, const float* s_up, const float* s_down,
+                             const void* s_gate, const void* s_up, const void* s_down,
                              float* y_sorted, void* workspace, size_t workspace_bytes,
                              void* stream);
 
@@ -293,8 +294,8 @@ size_t moe_layer_workspace_size(int T, int E, int k, int d, int d_ff, moe_dtype_
  */
 moe_status_t moe_layer(const float* logits, const void* x, moe_dtype_t act_dtype, int T, int E,
                        int k, int d, int d_ff, const void* w_gate, const void* w_up,
-                       const void* w_down, moe_dtype_t w_dtype, const float* s_gate,
-                       const float* s_up, const float* s_down, int32_t* topk_ids,
+                       const void* w_down, moe_dtype_t w_dtype, const void* s_gate,
+                       const void* s_up, const void* s_down, int32_t* topk_ids,
                        float* topk_gates, int32_t* counts, int32_t* offsets,
                        int32_t* sorted_to_flat, int32_t* flat_to_sorted, void* x_sorted,
                        float* y_sorted, void* y, moe_dtype_t y_dtype, void* workspace,
@@ -308,7 +309,7 @@ moe_status_t moe_layer(const float* logits, const void* x, moe_dtype_t act_dtype
 moe_status_t moe_layer_capped(const float* logits, const void* x, moe_dtype_t act_dtype, int T,
                               int E, int k, int d, int d_ff, int capacity, const void* w_gate,
                               const void* w_up, const void* w_down, moe_dtype_t w_dtype,
-                              const float* s_gate, const float* s_up, const float* s_down,
+                              const void* s_gate, const void* s_up, const void* s_down,
                               int32_t* topk_ids, float* topk_gates, int32_t* counts,
                               int32_t* offsets, int32_t* sorted_to_flat, int32_t* flat_to_sorted,
                               void* x_sorted, float* y_sorted, void* y, moe_dtype_t y_dtype,
@@ -483,7 +484,7 @@ moe_status_t moe_route_backward(const float* dgates, const int32_t* topk_ids,
  *   codes   [rows, d/2] bytes, row-major, element 2i in the low half of byte i;
  *   scales  [ceil(d/256), rows, 8] bytes: the scale of row r, elements 32 g .. 32 g + 31, at
  *           ((g / 8) * rows + r) * 8 + g % 8. (Scales stored [rows, d/32] elsewhere are brought into this order once.)
- *           Bytes of groups past d are never used; the library writes 127 there.
+ *           Bytes of groups past d (in the last block) are not used.
  * E matrices (weights [E, N, K]) lie one after the other, codes [E, N, K/2] and scales
  * [E, ceil(K/256), N, 8]. The values that the kernels work with are exact in fp32 for every byte, and in bf16 too.
  * Element counts may pass 2^32; a size whose kernels would need more than 2^32 threads gives MOE_ERR_UNSUPPORTED.
@@ -510,6 +511,41 @@ moe_status_t moe_mxfp4_quantize(const void* x, moe_dtype_t x_dtype, int E, int r
  */
 moe_status_t moe_mxfp4_dequantize(const void* codes, const void* scales, int E, int rows, int d,
                                   void* out, moe_dtype_t out_dtype, void* stream);
+
+/*
+ * moe_grouped_gemm_mxfp4 - moe_grouped_gemm with MXFP4 weights:
+ *     y[r] = W_e x[r]    for rows r in [offsets[e], offsets[e+1])
+ *
+ *   x        [rows, K] in x_dtype: MOE_BF16 (x_scales NULL), or MOE_MXFP4, codes with x_scales
+ *            [ceil(K/256), rows, 8]. (MOE_F32 and fp8: MOE_ERR_UNSUPPORTED.)
+ *   offsets  [E+1] int32, as moe_grouped_ffn; offsets[E] <= rows. Rows at or past offsets[E] are neither read
+ *            nor written.
+ *   w, w_scales  codes and scales of W [E, N, K]. Experts with no rows are never read.
+ *   y        [rows, N] out, in y_dtype (MOE_F32 or MOE_BF16, the fp32 sum rounded once).
+ *   Arithmetic: products of the values, summed in fp32. N a multiple of 8, K of 32, both at most 2^20.
+ */
+moe_status_t moe_grouped_gemm_mxfp4(const void* x, const void* x_scales, moe_dtype_t x_dtype,
+                                    const int32_t* offsets, int rows, int E, int N, int K,
+                                    const void* w, const void* w_scales, void* y,
+                                    moe_dtype_t y_dtype, void* stream);
+
+/*
+ * moe_grouped_swiglu_mxfp4 - gate and up products and the activation, in one launch:
+ *     h[r] = silu(Wg_e x[r]) * (Wu_e x[r]),  silu(z) = z/(1+e^-z)
+ *
+ *   x, x_scales, x_dtype, offsets  as moe_grouped_gemm_mxfp4, x [rows, d].
+ *   w_gate, gate_scales, w_up, up_scales  codes and scales of [E, d_ff, d] each.
+ *   h        [rows, d_ff] out, in h_dtype: MOE_BF16 (h_scales NULL), or MOE_MXFP4, codes with h_scales
+ *            [ceil(d_ff/256), rows, 8] as moe_mxfp4_quantize gives them for the fp32 result: what the
+ *            next product takes as its rows.
+ *   Arithmetic: both sums and the activation in fp32, one rounding to h_dtype. d and d_ff multiples of 32, at
+ *   most 2^20.
+ */
+moe_status_t moe_grouped_swiglu_mxfp4(const void* x, const void* x_scales, moe_dtype_t x_dtype,
+                                      const int32_t* offsets, int rows, int E, int d_ff, int d,
+                                      const void* w_gate, const void* gate_scales, const void* w_up,
+                                      const void* up_scales, void* h, void* h_scales,
+                                      moe_dtype_t h_dtype, void* stream);
 
 #ifdef __cplusplus
 }

@@ -22,7 +22,8 @@ MOE_F32, MOE_BF16, MOE_FP8_E4M3FN, MOE_BF16_BLOCKED, MOE_FP8_E4M3FN_BLOCKED = 0,
 MOE_MXFP4 = 16
 
 _DTYPE_ENUM = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16,
-               torch.float8_e4m3fn: MOE_FP8_E4M3FN, torch.uint8: MOE_FP8_E4M3FN}
+               torch.float8_e4m3fn: MOE_FP8_E4M3FN, torch.uint8: MOE_FP8_E4M3FN,
+               torch.float4_e2m1fn_x2: MOE_MXFP4}
 
 ENTRY_POINTS = (
     "moe_status_string", "moe_route", "moe_permute_workspace_size", "moe_permute",
@@ -33,6 +34,7 @@ ENTRY_POINTS = (
     "moe_grouped_gemm", "moe_grouped_gemm_dgrad", "moe_grouped_gemm_wgrad", "moe_checkpoint_pack",
     "moe_checkpoint_unpack", "moe_swiglu", "moe_swiglu_backward", "moe_combine_backward",
     "moe_permute_backward", "moe_route_backward", "moe_mxfp4_quantize", "moe_mxfp4_dequantize",
+    "moe_grouped_gemm_mxfp4", "moe_grouped_swiglu_mxfp4",
 )
 
 _lib = None
@@ -89,6 +91,8 @@ def load_library(path: str | None = None):
         "moe_route_backward": ([P, P, P, I, I, I, P, P], I),
         "moe_mxfp4_quantize": ([P, I, I, I, I, I, P, P, P, P], I),
         "moe_mxfp4_dequantize": ([P, P, I, I, I, P, I, P], I),
+        "moe_grouped_gemm_mxfp4": ([P, P, I, P, I, I, I, I, P, P, P, I, P], I),
+        "moe_grouped_swiglu_mxfp4": ([P, P, I, P, I, I, I, I, P, P, P, P, P, P, I, P], I),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -255,8 +259,20 @@ def moe_expert_capacity(T: int, E: int, k: int, factor_percent: int) -> int:
 
 def _weights(w_gate, w_up, w_down, s_gate, s_up, s_down, blocked=False):
     """blocked: the bf16 or fp8 weights are in their blocked layout (see moe_block_weights); the
-    tensors keep their [E, d_ff, d] / [E, d, d_ff] shapes."""
+    tensors keep their [E, d_ff, d] / [E, d, d_ff] shapes. MXFP4 weights are float4_e2m1fn_x2 codes, two to
+    an element of the tensors, with their scale bytes."""
     E, d_ff, d = w_gate.shape
+    if w_gate.dtype is torch.float4_e2m1fn_x2:
+        if blocked:
+            raise TypeError("blocked weights are bfloat16 or float8_e4m3fn")
+        d *= 2
+        for w, s, shp, n in ((w_gate, s_gate, (E, d_ff, d), "w_gate"), (w_up, s_up, (E, d_ff, d), "w_up"),
+                             (w_down, s_down, (E, d, d_ff), "w_down")):
+            if s is None:
+                raise ValueError(f"{n}: MXFP4 weights come with their scales")
+            _need(w, w_gate.dtype, (*shp[:2], shp[2] // 2), n)
+            _mx(w, s, shp, n)
+        return E, d, d_ff, MOE_MXFP4
     _need(w_up, w_gate.dtype, (E, d_ff, d), "w_up")
     _need(w_down, w_gate.dtype, (E, d, d_ff), "w_down")
     w_dt = _dt(w_gate, "w_gate")
@@ -626,6 +642,46 @@ def moe_mxfp4_dequantize(codes, scales, out, stream=None):
     _mx(codes, scales, shape, "codes")
     _call("moe_mxfp4_dequantize", stream, codes, scales, shape[0] if len(shape) == 3 else 1, *shape[-2:], out,
           _float_dt(out, "out"))
+
+
+def _mx_rows(x, x_scales, rows, K, name):
+    """The dtype of rows x: bfloat16, or codes (with scales)."""
+    if x_scales is None:
+        _need(x, torch.bfloat16, (rows, K), name)
+        return MOE_BF16
+    _mx(x, x_scales, (rows, K), name)
+    return MOE_MXFP4
+
+
+def moe_grouped_gemm_mxfp4(x, offsets, w, w_scales, y, x_scales=None, stream=None):
+    """y[r] = W_e x[r] for the rows of each expert e, with MXFP4 weights: w [E, N, K/2] codes and w_scales
+    [E, ceil(K/256), N, 8]. x [rows, K] bfloat16, or with x_scales [ceil(K/256), rows, 8] MXFP4 codes
+    [rows, K/2]; y [rows, N] float32 or bfloat16."""
+    rows = _dims(x, 2, "x")[0]
+    E, N, half = _dims(w, 3, "w")
+    K = 2 * half
+    x_dt = _mx_rows(x, x_scales, rows, K, "x")
+    _mx(w, w_scales, (E, N, K), "w")
+    _need(offsets, torch.int32, (E + 1,), "offsets")
+    _need(y, y.dtype, (rows, N), "y")
+    _call("moe_grouped_gemm_mxfp4", stream, x, x_scales, x_dt, offsets, rows, E, N, K, w, w_scales, y, _float_dt(y, "y"))
+
+
+def moe_grouped_swiglu_mxfp4(x, offsets, w_gate, gate_scales, w_up, up_scales, h, x_scales=None, h_scales=None,
+                             stream=None):
+    """h[r] = silu(Wg_e x[r]) * (Wu_e x[r]) with MXFP4 weights: codes [E, d_ff, d/2] and scales
+    [E, ceil(d/256), d_ff, 8]. x [rows, d] bfloat16, or MXFP4 codes with x_scales; h [rows, d_ff] bfloat16, or
+    MXFP4 codes [rows, d_ff/2] with h_scales [ceil(d_ff/256), rows, 8]."""
+    rows = _dims(x, 2, "x")[0]
+    E, d_ff, half = _dims(w_gate, 3, "w_gate")
+    d = 2 * half
+    x_dt = _mx_rows(x, x_scales, rows, d, "x")
+    _mx(w_gate, gate_scales, (E, d_ff, d), "w_gate")
+    _mx(w_up, up_scales, (E, d_ff, d), "w_up")
+    _need(offsets, torch.int32, (E + 1,), "offsets")
+    h_dt = _mx_rows(h, h_scales, rows, d_ff, "h")
+    _call("moe_grouped_swiglu_mxfp4", stream, x, x_scales, x_dt, offsets, rows, E, d_ff, d, w_gate, gate_scales, w_up,
+          up_scales, h, h_scales, h_dt)
 
 
 def layer_buffers(T: int, E: int, k: int, d: int, act_dtype, device="cuda",

@@ -134,7 +134,7 @@ moe_status_t check_permute(const void* x, moe_dtype_t x_dt, const int32_t* ids, 
 
 moe_status_t check_ffn(const void* x_sorted, moe_dtype_t act, const int32_t* offsets, int rows,
                        int E, int d, int d_ff, const void* wg, const void* wu, const void* wd,
-                       moe_dtype_t wdt, const float* sg, const float* su, const float* sd,
+                       moe_dtype_t wdt, const void* sg, const void* su, const void* sd,
                        const float* y_sorted, const void* ws, size_t ws_bytes) {
   if (rows < 0 || E < 1 || d < 1 || d_ff < 1 || d > kMaxDim || d_ff > kMaxDim)
     return MOE_ERR_INVALID_ARG;
@@ -143,13 +143,13 @@ moe_status_t check_ffn(const void* x_sorted, moe_dtype_t act, const int32_t* off
     if (wdt != MOE_F32) return MOE_ERR_UNSUPPORTED;
   } else if (act == MOE_BF16) {
     if (wdt != MOE_BF16 && wdt != MOE_FP8_E4M3FN && wdt != MOE_BF16_BLOCKED &&
-        wdt != MOE_FP8_E4M3FN_BLOCKED)
+        wdt != MOE_FP8_E4M3FN_BLOCKED && wdt != MOE_MXFP4)
       return MOE_ERR_UNSUPPORTED;
   } else {
     return MOE_ERR_UNSUPPORTED;
   }
   const bool fp8 = wdt == MOE_FP8_E4M3FN || wdt == MOE_FP8_E4M3FN_BLOCKED;
-  const int mult = fp8 ? 128 : (wdt == MOE_BF16_BLOCKED ? 64 : 8);
+  const int mult = fp8 ? 128 : (wdt == MOE_BF16_BLOCKED ? 64 : (wdt == MOE_MXFP4 ? 32 : 8));
   // blocked fp8 runs on the direct-to-LDS tiles only, which stage scales for contractions up to this
   if (wdt == MOE_FP8_E4M3FN_BLOCKED && (d > 65536 || d_ff > 65536)) return MOE_ERR_UNSUPPORTED;
   if (d % mult != 0 || d_ff % mult != 0) return MOE_ERR_UNSUPPORTED;
@@ -161,6 +161,9 @@ moe_status_t check_ffn(const void* x_sorted, moe_dtype_t act, const int32_t* off
   if (fp8) {
     const long long ns = (long long)E * (d / 128) * (d_ff / 128);
     if (!ok_ptr(sg, ns, 4) || !ok_ptr(su, ns, 4) || !ok_ptr(sd, ns, 4)) return MOE_ERR_INVALID_ARG;
+  } else if (wdt == MOE_MXFP4) {
+    if (!ok_ptr(sg, wel, 16) || !ok_ptr(su, wel, 16) || !ok_ptr(sd, wel, 16)) return MOE_ERR_INVALID_ARG;
+    if (!moe::mx_ffn_fits(rows, E, d, d_ff)) return MOE_ERR_UNSUPPORTED;
   } else if (sg || su || sd) {
     return MOE_ERR_INVALID_ARG;
   }
@@ -240,6 +243,40 @@ moe_status_t check_mx_width(int d) {
   return d % 32 == 0 ? MOE_OK : MOE_ERR_UNSUPPORTED;
 }
 long long mx_scale_bytes(long long rows, int d) { return (d + 255) / 256 * rows * 8; }
+
+// Rows x and weights of the products (the output is the caller's to check).
+moe_status_t check_mx_product(const moe::MxGemmArgs& a, moe_dtype_t x_dtype) {
+  const moe::GroupedGemmArgs& g = a.g;
+  if (x_dtype != MOE_BF16 && x_dtype != MOE_MXFP4)
+    return known_dtype(x_dtype) ? MOE_ERR_UNSUPPORTED : MOE_ERR_INVALID_ARG;
+  if (g.E > MOE_MAX_EXPERTS) return MOE_ERR_UNSUPPORTED;
+  const long long R = g.rows, W = (long long)g.E * g.N * g.K;
+  if (!ok_ptr(g.a, R * g.K, 16) || !ok_ptr(g.b, W, 16) || !ok_ptr(a.b_scales, W, 16) || !ok_ptr(g.offsets, g.E + 1, 4))
+    return MOE_ERR_INVALID_ARG;
+  if (x_dtype == MOE_MXFP4 ? !ok_ptr(a.a_scales, R, 16) : a.a_scales != nullptr) return MOE_ERR_INVALID_ARG;
+  return moe::mx_gemm_fits(a) ? MOE_OK : MOE_ERR_UNSUPPORTED;
+}
+
+// The grouped FFN of checked arguments: with MXFP4 weights gate, up and SwiGLU in one launch, down in another.
+hipError_t launch_ffn(const void* x_sorted, moe_dtype_t act, const int32_t* offsets, int rows, int E, int d, int d_ff,
+                      const void* w_gate, const void* w_up, const void* w_down, moe_dtype_t w_dtype,
+                      const void* s_gate, const void* s_up, const void* s_down, float* y_sorted, void* workspace,
+                      const moe::DeviceInfo& dev, hipStream_t stream) {
+  if (w_dtype != MOE_MXFP4) {
+    const moe::FfnArgs a{x_sorted, act, offsets, rows, E, d, d_ff, w_gate, w_up, w_down, w_dtype,
+                         static_cast<const float*>(s_gate), static_cast<const float*>(s_up),
+                         static_cast<const float*>(s_down), y_sorted, workspace};
+    return moe::launch_grouped_ffn(a, dev, stream);
+  }
+  if (rows == 0) return hipSuccess;
+  const moe::MxGemmArgs up{{x_sorted, w_gate, nullptr, w_up, workspace, offsets, rows, E, d_ff, d, true, true, false},
+                           false, nullptr, static_cast<const uint8_t*>(s_gate), static_cast<const uint8_t*>(s_up), nullptr};
+  const hipError_t e = moe::launch_mx_gemm(up, stream);
+  if (e != hipSuccess) return e;
+  const moe::MxGemmArgs down{{workspace, w_down, nullptr, nullptr, y_sorted, offsets, rows, E, d, d_ff, true, false, false},
+                             false, nullptr, static_cast<const uint8_t*>(s_down), nullptr, nullptr};
+  return moe::launch_mx_gemm(down, stream);
+}
 
 moe_status_t hip_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
 
@@ -352,13 +389,14 @@ size_t moe_ffn_workspace_size(int rows, int E, int d, int d_ff, moe_dtype_t act_
                               moe_dtype_t w_dtype) {
   if (rows < 0 || E < 1 || d < 1 || d_ff < 1 || d > kMaxDim || d_ff > kMaxDim) return 0;
   if (act_dtype != MOE_F32 && act_dtype != MOE_BF16) return 0;
+  if (w_dtype == MOE_MXFP4) return align_up((size_t)rows * d_ff * act_bytes(act_dtype), 256);  // h
   return moe::ffn_workspace_bytes(rows, E, d, d_ff, act_dtype, w_dtype);
 }
 
 moe_status_t moe_grouped_ffn(const void* x_sorted, moe_dtype_t act_dtype, const int32_t* offsets,
                              int rows, int E, int d, int d_ff, const void* w_gate,
                              const void* w_up, const void* w_down, moe_dtype_t w_dtype,
-                             const float* s_gate, const float* s_up, const float* s_down,
+                             const void* s_gate, const void* s_up, const void* s_down,
                              float* y_sorted, void* workspace, size_t workspace_bytes,
                              void* stream) {
   moe_status_t s = check_ffn(x_sorted, act_dtype, offsets, rows, E, d, d_ff, w_gate, w_up, w_down,
@@ -368,9 +406,8 @@ moe_status_t moe_grouped_ffn(const void* x_sorted, moe_dtype_t act_dtype, const 
   moe::DeviceInfo dev;
   hipError_t e = moe::device_info(&dev);
   if (e != hipSuccess) return MOE_ERR_HIP;
-  moe::FfnArgs a{x_sorted, act_dtype, offsets, rows, E, d, d_ff, w_gate, w_up, w_down,
-                 w_dtype, s_gate, s_up, s_down, y_sorted, workspace};
-  return hip_status(moe::launch_grouped_ffn(a, dev, static_cast<hipStream_t>(stream)));
+  return hip_status(launch_ffn(x_sorted, act_dtype, offsets, rows, E, d, d_ff, w_gate, w_up, w_down, w_dtype, s_gate,
+                               s_up, s_down, y_sorted, workspace, dev, static_cast<hipStream_t>(stream)));
 }
 
 moe_status_t moe_block_weights(const void* src, void* dst, moe_dtype_t w_dtype, int E, int N, int K,
@@ -408,8 +445,8 @@ size_t moe_layer_workspace_size(int T, int E, int k, int d, int d_ff, moe_dtype_
 
 moe_status_t moe_layer_capped(const float* logits, const void* x, moe_dtype_t act_dtype, int T,
                               int E, int k, int d, int d_ff, int capacity, const void* w_gate, const void* w_up,
-                       const void* w_down, moe_dtype_t w_dtype, const float* s_gate,
-                       const float* s_up, const float* s_down, int32_t* topk_ids,
+                       const void* w_down, moe_dtype_t w_dtype, const void* s_gate,
+                       const void* s_up, const void* s_down, int32_t* topk_ids,
                        float* topk_gates, int32_t* counts, int32_t* offsets,
                        int32_t* sorted_to_flat, int32_t* flat_to_sorted, void* x_sorted,
                        float* y_sorted, void* y, moe_dtype_t y_dtype, void* workspace,
@@ -441,17 +478,17 @@ moe_status_t moe_layer_capped(const float* logits, const void* x, moe_dtype_t ac
                           sorted_to_flat, flat_to_sorted, x_sorted,
                           reinterpret_cast<int32_t*>(wsb), st) != hipSuccess)
     return MOE_ERR_HIP;
-  moe::FfnArgs a{x_sorted, act_dtype, offsets, T * k, E, d, d_ff, w_gate, w_up, w_down,
-                 w_dtype, s_gate, s_up, s_down, y_sorted, wsb + ws_perm};
-  if (moe::launch_grouped_ffn(a, dev, st) != hipSuccess) return MOE_ERR_HIP;
+  if (launch_ffn(x_sorted, act_dtype, offsets, T * k, E, d, d_ff, w_gate, w_up, w_down, w_dtype, s_gate, s_up, s_down,
+                 y_sorted, wsb + ws_perm, dev, st) != hipSuccess)
+    return MOE_ERR_HIP;
   return hip_status(moe::launch_combine(y_sorted, flat_to_sorted, topk_gates, T, k, d, y,
                                         y_dtype == MOE_BF16, st));
 }
 
 moe_status_t moe_layer(const float* logits, const void* x, moe_dtype_t act_dtype, int T, int E,
                        int k, int d, int d_ff, const void* w_gate, const void* w_up,
-                       const void* w_down, moe_dtype_t w_dtype, const float* s_gate,
-                       const float* s_up, const float* s_down, int32_t* topk_ids,
+                       const void* w_down, moe_dtype_t w_dtype, const void* s_gate,
+                       const void* s_up, const void* s_down, int32_t* topk_ids,
                        float* topk_gates, int32_t* counts, int32_t* offsets,
                        int32_t* sorted_to_flat, int32_t* flat_to_sorted, void* x_sorted,
                        float* y_sorted, void* y, moe_dtype_t y_dtype, void* workspace,
@@ -644,6 +681,49 @@ moe_status_t moe_mxfp4_dequantize(const void* codes, const void* scales, int E, 
   if (moe::mx_row_grid(n, d) > moe::kMaxWorkgroups) return MOE_ERR_UNSUPPORTED;
   return hip_status(moe::launch_mx_dequantize(codes, scales, E, rows, d, out, out_dtype == MOE_BF16,
                                               static_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_grouped_gemm_mxfp4(const void* x, const void* x_scales, moe_dtype_t x_dtype,
+                                    const int32_t* offsets, int rows, int E, int N, int K,
+                                    const void* w, const void* w_scales, void* y,
+                                    moe_dtype_t y_dtype, void* stream) {
+  if (rows < 0 || E < 1) return MOE_ERR_INVALID_ARG;
+  moe_status_t s = check_width(N);
+  if (s == MOE_OK) s = check_mx_width(K);
+  if (s == MOE_OK) s = check_float_dtype(y_dtype);
+  if (s != MOE_OK) return s;
+  const moe::MxGemmArgs a{{x, w, nullptr, nullptr, y, offsets, rows, E, N, K, true, y_dtype == MOE_BF16, false},
+                          x_dtype == MOE_MXFP4, static_cast<const uint8_t*>(x_scales),
+                          static_cast<const uint8_t*>(w_scales), nullptr, nullptr};
+  s = check_mx_product(a, x_dtype);
+  if (s != MOE_OK) return s;
+  if (!ok_ptr(y, (long long)rows * N, 16)) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  return hip_status(moe::launch_mx_gemm(a, static_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_grouped_swiglu_mxfp4(const void* x, const void* x_scales, moe_dtype_t x_dtype,
+                                      const int32_t* offsets, int rows, int E, int d_ff, int d,
+                                      const void* w_gate, const void* gate_scales, const void* w_up,
+                                      const void* up_scales, void* h, void* h_scales,
+                                      moe_dtype_t h_dtype, void* stream) {
+  if (rows < 0 || E < 1) return MOE_ERR_INVALID_ARG;
+  moe_status_t s = check_mx_width(d_ff);
+  if (s == MOE_OK) s = check_mx_width(d);
+  if (s != MOE_OK) return s;
+  if (h_dtype != MOE_BF16 && h_dtype != MOE_MXFP4)
+    return known_dtype(h_dtype) ? MOE_ERR_UNSUPPORTED : MOE_ERR_INVALID_ARG;
+  const moe::MxGemmArgs a{{x, w_gate, nullptr, w_up, h, offsets, rows, E, d_ff, d, true, true, false},
+                          x_dtype == MOE_MXFP4, static_cast<const uint8_t*>(x_scales),
+                          static_cast<const uint8_t*>(gate_scales), static_cast<const uint8_t*>(up_scales),
+                          static_cast<uint8_t*>(h_scales)};
+  s = check_mx_product(a, x_dtype);
+  if (s != MOE_OK) return s;
+  const long long R = rows;
+  if (!ok_ptr(w_up, 1, 16) || !ok_ptr(up_scales, 1, 16) || !ok_ptr(h, R * d_ff, 16)) return MOE_ERR_INVALID_ARG;
+  if (h_dtype == MOE_MXFP4 ? !ok_ptr(h_scales, R, 16) : h_scales != nullptr) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  return hip_status(moe::launch_mx_gemm(a, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"
