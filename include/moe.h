@@ -530,6 +530,22 @@ moe_status_t moe_grouped_gemm_mxfp4(const void* x, const void* x_scales, moe_dty
                                     moe_dtype_t y_dtype, void* stream);
 
 /*
+ * moe_grouped_gemm_mxfp4_dgrad - its gradient with respect to x, for training through weights that stay as they are:
+ *     dx[r] = W_e^T dy[r]  (+ W2_e^T dy2[r])
+ *
+ *   dy       [rows, N] in dy_dtype, MOE_BF16 (others: MOE_ERR_UNSUPPORTED); dy2: a second gradient of the
+ *            same shape, or NULL.
+ *   w, w_scales  the forward product's weights as they are held; w2, w2_scales: those of dy2, NULL exactly
+ *            when dy2 is. Both products go into one fp32 sum.
+ *   dx       [rows, K] out, in dx_dtype (MOE_F32 or MOE_BF16).
+ */
+moe_status_t moe_grouped_gemm_mxfp4_dgrad(const void* dy, const void* dy2, moe_dtype_t dy_dtype,
+                                          const int32_t* offsets, int rows, int E, int N, int K,
+                                          const void* w, const void* w_scales, const void* w2,
+                                          const void* w2_scales, void* dx, moe_dtype_t dx_dtype,
+                                          void* stream);
+
+/*
  * moe_grouped_swiglu_mxfp4 - gate and up products and the activation, in one launch:
  *     h[r] = silu(Wg_e x[r]) * (Wu_e x[r]),  silu(z) = z/(1+e^-z)
  *

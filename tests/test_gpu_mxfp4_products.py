@@ -75,6 +75,66 @@ def test_product(dev, counts, N, K, kind, out):
     assert ((y[:used].double() - want).abs() <= tol).all()
 
 
+@pytest.mark.parametrize("pair", [False, True])
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("N, K", [(8, 32), (40, 96), (264, 800), (128, 256), (1544, 1056), (4104, 544)])
+@pytest.mark.parametrize("counts", COUNTS, ids=lambda c: "-".join(map(str, c)))
+def test_input_gradient(dev, counts, N, K, out, pair):
+    used, E = sum(counts), len(counts)
+    rows = used + 5
+    weights = [held((E, N, K), dev, 1 + i, K ** -0.5) for i in range(1 + pair)]
+    dys = [rows_in("bf16", rows, N, dev, 7 + i, used)[0] for i in range(1 + pair)]
+    more = dict(dy2=dys[1], w2=weights[1][0], w2_scales=weights[1][1]) if pair else {}
+    dx, whole = ref.guarded((rows, K), out, dev)
+    moe.moe_grouped_gemm_mxfp4_dgrad(dys[0], ref.offsets_of(counts, dev), weights[0][0], weights[0][1], dx, **more)
+    torch.cuda.synchronize()
+    assert ref.guards_intact(whole, rows * K)
+    assert torch.isnan(dx[used:]).all()
+    want = e = 0
+    for (_, _, wv), dy in zip(weights, dys):
+        across = wv.transpose(1, 2).contiguous()
+        want = want + ref.forward(dy[:used], across, counts)
+        e = e + (1 + pair) * N * 2.0 ** -23 * ref.forward(dy[:used].abs(), across.abs(), counts)
+    tol = e + ref.u(out) * (want.abs() + e) + 1e-37
+    assert ((dx[:used].double() - want).abs() <= tol).all()
+
+
+def test_input_gradient_nan(dev):
+    """A NaN group of W reaches its 32 columns of that expert's rows alone, a NaN in dy its row."""
+    counts, N, K = [20, 300], 72, 544
+    w, ws, _ = held((2, N, K), dev, 1)
+    ws[1, 1, 7, 3] = 255                      # expert 1, row 7, columns 352 .. 383
+    dy = rows_in("bf16", 320, N, dev, 2, 320)[0]
+    dy[2, 70] = float("nan")
+    dx = torch.zeros((320, K), device=dev)
+    moe.moe_grouped_gemm_mxfp4_dgrad(dy, ref.offsets_of(counts, dev), w, ws, dx)
+    want = torch.zeros_like(dx, dtype=torch.bool)
+    want[2] = True
+    want[20:, 352:384] = True
+    assert torch.equal(torch.isnan(dx), want)
+
+
+def test_input_gradient_by_differences(dev):
+    """The gradient is that of the forward call: linear, so a difference along any direction is exact but for rounding."""
+    counts, N, K = [9, 0, 30], 96, 160
+    w, ws, wv = held((3, N, K), dev, 1, K ** -0.5)
+    offsets = ref.offsets_of(counts, dev)
+    x, _, xv = rows_in("bf16", 39, K, dev, 2, 39)
+    dy, _, dyv = rows_in("bf16", 39, N, dev, 3, 39)
+    step, _, sv = rows_in("bf16", 39, K, dev, 4, 39)
+    y0, y1, dx = (torch.empty((39, n), device=dev) for n in (N, N, K))
+    both = (x.float() + step.float()).to(BF)
+    moe.moe_grouped_gemm_mxfp4(x, offsets, w, ws, y0)
+    moe.moe_grouped_gemm_mxfp4(both, offsets, w, ws, y1)
+    moe.moe_grouped_gemm_mxfp4_dgrad(dy, offsets, w, ws, dx)
+    moved = both.double() - xv                # what the step became in bf16
+    left = ((y1.double() - y0.double()) * dyv).sum(1)
+    right = (dx.double() * moved).sum(1)
+    size = ((ref.forward(both.double().abs(), wv.abs(), counts) + ref.forward(xv.abs(), wv.abs(), counts)) * dyv.abs()).sum(1)
+    back = (ref.forward(dyv.abs(), wv.abs().transpose(1, 2).contiguous(), counts) * moved.abs()).sum(1)
+    assert ((left - right).abs() <= (K + 1) * 2.0 ** -23 * size + (N + 1) * 2.0 ** -23 * back).all()
+
+
 def silu(g):
     return g * torch.sigmoid(g)
 

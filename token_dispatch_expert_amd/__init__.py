@@ -11,5 +11,6 @@ from .binding import (  # noqa: F401
     moe_block_weights, moe_checkpoint_pack, moe_checkpoint_unpack, moe_combine_backward,
     moe_grouped_gemm, moe_grouped_gemm_dgrad, moe_grouped_gemm_wgrad, moe_permute_backward,
     moe_route_backward, moe_swiglu, moe_swiglu_backward, moe_mxfp4_quantize,
-    moe_mxfp4_dequantize, mxfp4_buffers, moe_grouped_gemm_mxfp4, moe_grouped_swiglu_mxfp4,
+    moe_mxfp4_dequantize, mxfp4_buffers, moe_grouped_gemm_mxfp4,
+    moe_grouped_gemm_mxfp4_dgrad, moe_grouped_swiglu_mxfp4,
 )

@@ -34,7 +34,7 @@ ENTRY_POINTS = (
     "moe_grouped_gemm", "moe_grouped_gemm_dgrad", "moe_grouped_gemm_wgrad", "moe_checkpoint_pack",
     "moe_checkpoint_unpack", "moe_swiglu", "moe_swiglu_backward", "moe_combine_backward",
     "moe_permute_backward", "moe_route_backward", "moe_mxfp4_quantize", "moe_mxfp4_dequantize",
-    "moe_grouped_gemm_mxfp4", "moe_grouped_swiglu_mxfp4",
+    "moe_grouped_gemm_mxfp4", "moe_grouped_gemm_mxfp4_dgrad", "moe_grouped_swiglu_mxfp4",
 )
 
 _lib = None
@@ -92,6 +92,7 @@ def load_library(path: str | None = None):
         "moe_mxfp4_quantize": ([P, I, I, I, I, I, P, P, P, P], I),
         "moe_mxfp4_dequantize": ([P, P, I, I, I, P, I, P], I),
         "moe_grouped_gemm_mxfp4": ([P, P, I, P, I, I, I, I, P, P, P, I, P], I),
+        "moe_grouped_gemm_mxfp4_dgrad": ([P, P, I, P, I, I, I, I, P, P, P, P, P, I, P], I),
         "moe_grouped_swiglu_mxfp4": ([P, P, I, P, I, I, I, I, P, P, P, P, P, P, I, P], I),
     }
     for name, (args, res) in sig.items():
@@ -665,6 +666,25 @@ def moe_grouped_gemm_mxfp4(x, offsets, w, w_scales, y, x_scales=None, stream=Non
     _need(offsets, torch.int32, (E + 1,), "offsets")
     _need(y, y.dtype, (rows, N), "y")
     _call("moe_grouped_gemm_mxfp4", stream, x, x_scales, x_dt, offsets, rows, E, N, K, w, w_scales, y, _float_dt(y, "y"))
+
+
+def moe_grouped_gemm_mxfp4_dgrad(dy, offsets, w, w_scales, dx, dy2=None, w2=None, w2_scales=None, stream=None):
+    """dx[r] = W_e^T dy[r], plus W2_e^T dy2[r] with dy2, w2 and w2_scales. dy [rows, N] bfloat16, w and w_scales as the
+    forward product takes them, dx [rows, K] float32 or bfloat16."""
+    rows, N = _dims(dy, 2, "dy")
+    E, _, half = _dims(w, 3, "w")
+    K = 2 * half
+    _need(dy, torch.bfloat16, (rows, N), "dy")
+    _mx(w, w_scales, (E, N, K), "w")
+    _need(offsets, torch.int32, (E + 1,), "offsets")
+    _need(dx, dx.dtype, (rows, K), "dx")
+    if not (dy2 is None and w2 is None and w2_scales is None):
+        if dy2 is None or w2 is None or w2_scales is None:
+            raise ValueError("dy2, w2 and w2_scales come together")
+        _need(dy2, dy.dtype, (rows, N), "dy2")
+        _mx(w2, w2_scales, (E, N, K), "w2")
+    _call("moe_grouped_gemm_mxfp4_dgrad", stream, dy, dy2, MOE_BF16, offsets, rows, E, N, K, w, w_scales, w2, w2_scales,
+          dx, _float_dt(dx, "dx"))
 
 
 def moe_grouped_swiglu_mxfp4(x, offsets, w_gate, gate_scales, w_up, up_scales, h, x_scales=None, h_scales=None,

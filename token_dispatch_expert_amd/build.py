@@ -18,7 +18,7 @@ ARCH = os.environ.get("MOE_OFFLOAD_ARCH", "gfx950")
 
 SOURCES = ["route.hip", "router.hip", "permute.hip", "ffn.hip", "combine.hip", "layout.hip",
            "grouped_gemm.hip", "checkpoint.hip", "backward.hip", "mxfp4.hip",
-           "mxfp4_gemm.hip", "api.cpp"]
+           "mxfp4_gemm.hip", "mxfp4_dgrad.hip", "api.cpp"]
 
 # Packed fp32 VALU ops are disabled for all device code; the host pass ignores the feature.
 FLAGS = [

@@ -726,4 +726,30 @@ moe_status_t moe_grouped_swiglu_mxfp4(const void* x, const void* x_scales, moe_d
   return hip_status(moe::launch_mx_gemm(a, static_cast<hipStream_t>(stream)));
 }
 
+moe_status_t moe_grouped_gemm_mxfp4_dgrad(const void* dy, const void* dy2, moe_dtype_t dy_dtype,
+                                          const int32_t* offsets, int rows, int E, int N, int K,
+                                          const void* w, const void* w_scales, const void* w2,
+                                          const void* w2_scales, void* dx, moe_dtype_t dx_dtype,
+                                          void* stream) {
+  if (rows < 0 || E < 1) return MOE_ERR_INVALID_ARG;
+  moe_status_t s = check_width(N);
+  if (s == MOE_OK) s = check_mx_width(K);
+  if (s == MOE_OK) s = check_float_dtype(dx_dtype);
+  if (s != MOE_OK) return s;
+  if (dy_dtype != MOE_BF16) return known_dtype(dy_dtype) ? MOE_ERR_UNSUPPORTED : MOE_ERR_INVALID_ARG;
+  if (E > MOE_MAX_EXPERTS) return MOE_ERR_UNSUPPORTED;
+  const long long R = rows, W = (long long)E * N * K;
+  if (!ok_ptr(dy, R * N, 16) || !ok_ptr(w, W, 16) || !ok_ptr(w_scales, W, 16) || !ok_ptr(dx, R * K, 16) ||
+      !ok_ptr(offsets, E + 1, 4))
+    return MOE_ERR_INVALID_ARG;
+  if ((w2 == nullptr) != (w2_scales == nullptr) || (R > 0 && (dy2 == nullptr) != (w2 == nullptr)))
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned(dy2, 16) || !aligned(w2, 16) || !aligned(w2_scales, 16)) return MOE_ERR_INVALID_ARG;
+  const moe::MxGemmArgs a{{dy, w, dy2, w2, dx, offsets, rows, E, N, K, true, dx_dtype == MOE_BF16, false}, false, nullptr,
+                          static_cast<const uint8_t*>(w_scales), static_cast<const uint8_t*>(w2_scales), nullptr};
+  if (!moe::mx_dgrad_fits(a)) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  return hip_status(moe::launch_mx_dgrad(a, static_cast<hipStream_t>(stream)));
+}
+
 }  // extern "C"

@@ -1,0 +1,200 @@
+// The input gradient of the products with MXFP4 weights: dx[r] = W_e^T dy[r] (+ W2_e^T dy2[r]).
+//
+// The contraction runs over W's rows, while codes and scales lie along them, so the matrix instructions cannot take the
+// codes as they are stored. A step's weights are converted to bf16 on their way into LDS instead, exactly, where they lie
+// as bf16 weights would, and the transposing LDS reads of the bf16 input gradient bring them to the matrix
+// instructions: the codes move a quarter of the bytes from HBM, and the products run at the bf16 rate.
+#include "mxfp4.h"
+#include "mxfp4_internal.h"
+#include "product_tiles.h"
+
+namespace moe {
+
+namespace {
+
+struct MxDgradArgs {
+  ProductArgs p;  // a: dy, b: W's codes; a2, b2: the second pair, or null
+  const uint8_t *scales, *scales2;
+};
+
+// Steps of DK rows of W: each thread loads CPT chunks of 16 bytes (32 columns of a row) with their scale bytes, a step before
+// it converts and writes them into the image that Operand<true, ..> reads.
+template <int TN, int DK, int NT>
+struct Codes {
+  static constexpr int kRowChunks = TN / 32, CPT = DK * kRowChunks / NT, kRowsPerPass = NT / kRowChunks;
+  static_assert(CPT >= 1 && CPT * NT == DK * kRowChunks && kMxBlock % TN == 0, "chunks split evenly over the threads");
+  using Image = Operand<true, TN, DK, NT / 64>;
+  const char* base;       // the tile's first column in W's row 0
+  const uint8_t* scales;  // of W's row 0, in the block that holds the tile's columns
+  int ld, col, row, part; // bytes of a row; bytes before the tile's first column; this thread's first row and chunk
+  u32x4 c[CPT];
+  unsigned s[CPT];
+
+  __device__ __forceinline__ void set(const MxDgradArgs& a, int e, int c0) {
+    const ProductArgs& p = a.p;
+    ld = p.K / 2;
+    col = c0 / 2;
+    base = static_cast<const char*>(p.b) + (size_t)e * p.N * ld + col;
+    row = threadIdx.x / kRowChunks;
+    part = threadIdx.x % kRowChunks;
+    scales = a.scales + mx_scale_at(e, mx_blocks(p.K), c0 / kMxBlock, p.N, 0) + (c0 & (kMxBlock - 1)) / kMxGroup;
+  }
+  // rows k0 .. k0 + DK - 1 of W (of N); rows past the last are zeros. What a tile's columns past K read is
+  // in bounds and meets only columns of dx that do not exist.
+  __device__ __forceinline__ void load(int k0, int N, ptrdiff_t moved, ptrdiff_t scales_moved) {
+    const int left = N - k0;
+    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)(base + moved + (size_t)k0 * ld), (short)0,
+                                                                       min(DK, left) * ld - col, kBufferWord3);
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)(scales + scales_moved + (size_t)k0 * 8), (short)0, min(DK, left) * 8, kBufferWord3);
+#pragma unroll
+    for (int i = 0; i < CPT; ++i) {
+      const int n = row + i * kRowsPerPass;
+      c[i] = __builtin_amdgcn_raw_buffer_load_b128(r, n * ld + part * 16, 0, 0);
+      s[i] = (unsigned char)__builtin_amdgcn_raw_buffer_load_b8(rs, n * 8 + part, 0, 0);
+    }
+  }
+  __device__ __forceinline__ void put(u32x4* slot) const {
+#pragma unroll
+    for (int i = 0; i < CPT; ++i) {
+      const int n = row + i * kRowsPerPass;
+      const float scale = mx_scale_f32(s[i]);
+      char* const to = reinterpret_cast<char*>(slot) + n * (TN * 2);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<bf16x8*>(to + ((part * 2 + (q >> 1)) ^ Image::unit(n)) * 32 + (q & 1) * 16) =
+            mx_bf16x8(c[i][q], scale);
+    }
+  }
+};
+
+// As tile_kernel of the bf16 products (grouped_gemm.hip), with W through registers.
+template <int WM, int WN, int WGM, int WGN, int DK, int RING, bool DEAL>
+__global__ __launch_bounds__(64 * WGM * WGN) void mx_dgrad_kernel(MxDgradArgs a) {
+  constexpr int TM = WM * WGM, TN = WN * WGN, NW = WGM * WGN;
+  constexpr int MF = WM / 16, NF = WN / 16, NS = DK / 32;
+  using OA = Operand<false, TM, DK, NW>;
+  using OB = Operand<true, TN, DK, NW>;
+  constexpr int STAGE = OA::kChunks + OB::kChunks, LOADS = OA::kLoads;
+  static_assert(RING * STAGE * 16 <= 160 * 1024, "LDS");
+  __shared__ __align__(16) u32x4 ring[RING * STAGE];
+  const ProductArgs& p = a.p;
+  TileAt t;
+  if (!tile_at<kDgrad, DEAL>(p, TM, TN, t)) return;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / WGN * WM, wn = wave % WGN * WN;
+
+  OA oa;
+  Codes<TN, DK, 64 * NW> codes;
+  oa.set(static_cast<const __bf16*>(p.a) + (size_t)t.ra * p.N, t.m0, t.mlim, p.N, wave, lane);
+  codes.set(a, t.e, t.c0);
+  const bool pair = p.a2 != nullptr;
+  const ptrdiff_t moved_a = pair ? static_cast<const char*>(p.a2) - static_cast<const char*>(p.a) : 0;
+  const ptrdiff_t moved_b = pair ? static_cast<const char*>(p.b2) - static_cast<const char*>(p.b) : 0;
+  const ptrdiff_t moved_s = pair ? a.scales2 - a.scales : 0;
+  const int steps1 = (t.kdim + DK - 1) / DK, steps = pair ? 2 * steps1 : steps1;
+
+  auto issue = [&](int st) __attribute__((always_inline)) {
+    const bool second = st >= steps1;
+    oa.template issue<0>(ring + st % RING * STAGE, (second ? st - steps1 : st) * DK, t.kdim, second ? moved_a : 0, wave);
+  };
+  auto load = [&](int st) __attribute__((always_inline)) {
+    const bool second = st >= steps1;
+    codes.load((second ? st - steps1 : st) * DK, t.kdim, second ? moved_b : 0, second ? moved_s : 0);
+  };
+  auto run = [&](auto present) __attribute__((always_inline)) {
+    constexpr int F = decltype(present)::value;
+    f32x4 acc[F ? F : 1][NF];
+#pragma unroll
+    for (int i = 0; i < F; ++i)
+#pragma unroll
+      for (int j = 0; j < NF; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    bf16x8 fa[F ? F : 1], fb[2][NF];
+#pragma unroll
+    for (int r = 0; r < RING; ++r)
+      if (r < steps) {
+        load(r);
+        issue(r);
+        codes.put(ring + r * STAGE + OA::kChunks);
+      }
+    if (RING < steps) load(RING);
+    wait_vmcnt<0>();
+    wait_lgkmcnt0();
+    bare_barrier();
+#pragma unroll
+    for (int j = 0; j < (F ? NF : 0); ++j) fb[0][j] = OB::read(ring + OA::kChunks, wn + j * 16, 0, lane);
+#pragma unroll
+    for (int i = 0; i < F; ++i) fa[i] = OA::read(ring, wm + i * 16, 0, lane);
+    for (int st = 0; st < steps; ++st) {
+      u32x4* slot = ring + st % RING * STAGE;
+      const u32x4* next = ring + (st + 1) % RING * STAGE;
+      static_for<NS>([&](auto hc) __attribute__((always_inline)) {
+        constexpr int h = decltype(hc)::value, cur = h & 1;
+        if (h == NS - 1) {
+          wait_lgkmcnt0();  // this wave's reads of step st are back, its weights of later steps written
+          if (st + 1 < steps) {
+            // step st + 1 has landed for this wave, and after the barrier for all; all are done with step st's slot
+            wait_steps<LOADS, RING - 2>(steps - 2 - st);
+            bare_barrier();
+            if (st + RING < steps) {
+              codes.put(slot + OA::kChunks);
+              if (st + RING + 1 < steps) load(st + RING + 1);
+              issue(st + RING);
+            }
+          }
+        }
+        // Past the last step these reads bring nothing that is used (any slot, in bounds).
+        const u32x4* rs = h + 1 < NS ? slot : next;
+        constexpr int rh = (h + 1) % NS;
+#pragma unroll
+        for (int j = 0; j < (F ? NF : 0); ++j) fb[cur ^ 1][j] = OB::read(rs + OA::kChunks, wn + j * 16, rh, lane);
+#pragma unroll
+        for (int i = 0; i < F; ++i) {
+#pragma unroll
+          for (int j = 0; j < NF; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[cur][j], fa[i], acc[i][j], 0, 0, 0);
+          fa[i] = OA::read(rs, wm + i * 16, rh, lane);
+        }
+        __atomic_signal_fence(__ATOMIC_SEQ_CST);  // the reads stay in this slice
+      });
+    }
+    OutTile o;
+    o.set(p, (size_t)t.ra + t.m0, t.mlim, t.c0, t.clim, p.K);
+#pragma unroll
+    for (int i = 0; i < F; ++i) store_fragments<NF>(o, p, acc[i], wm + i * 16, wn, lane);
+  };
+  if constexpr (DEAL) {
+    const int mine = __builtin_amdgcn_readfirstlane(min(MF, max(0, (t.mlim - wm + 15) / 16)));
+    static_for<MF + 1>([&](auto c) __attribute__((always_inline)) {
+      if (mine == decltype(c)::value) run(c);
+    });
+  } else {
+    run(std::integral_constant<int, MF>{});
+  }
+}
+
+template <int WM, int WN, int WGM, int WGN, int DK, int RING, bool DEAL>
+hipError_t launch_tiles(const GroupedGemmArgs& g, const MxDgradArgs& p, hipStream_t stream) {
+  const long long grid = xcd_grid(tile_items(kDgrad, g, WM * WGM, WN * WGN));
+  mx_dgrad_kernel<WM, WN, WGM, WGN, DK, RING, DEAL><<<(unsigned)grid, 64 * WGM * WGN, 0, stream>>>(p);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+bool mx_dgrad_fits(const MxGemmArgs& a) {
+  return xcd_grid(tile_items(kDgrad, a.g, 32, 128)) <= kMaxWorkgroups / 2;
+}
+
+hipError_t launch_mx_dgrad(const MxGemmArgs& a, hipStream_t stream) {
+  const GroupedGemmArgs& g = a.g;
+  const MxDgradArgs p{{g.a, g.b, g.a2, g.b2, g.out, g.offsets, g.rows, g.E, g.N, g.K, g.out_bf16 ? 1 : 0, 0,
+                       stream_rows(g, kDgrad)},
+                      a.b_scales, a.b2_scales};
+  const long long mean = g.rows / g.E;
+  if (mean >= 128) return launch_tiles<128, 64, 2, 4, 64, 2, true>(g, p, stream);
+  return launch_tiles<32, 32, 1, 4, 64, 3, false>(g, p, stream);
+}
+
+}  // namespace moe

@@ -25,5 +25,9 @@ struct MxGemmArgs {
 bool mx_gemm_fits(const MxGemmArgs& a);
 bool mx_ffn_fits(int rows, int E, int d, int d_ff);  // the products of a grouped FFN
 hipError_t launch_mx_gemm(const MxGemmArgs& a, hipStream_t stream);
+// Their input gradient: g.a = dy [rows, N] in bf16, g.b = W's codes with b_scales, g.a2, g.b2 and b2_scales a second pair
+// or null; g.out = dx [rows, K].
+bool mx_dgrad_fits(const MxGemmArgs& a);
+hipError_t launch_mx_dgrad(const MxGemmArgs& a, hipStream_t stream);
 
 }  // namespace moe
