@@ -6,10 +6,8 @@
 // with its scale. Weights that meet bf16 rows are converted in registers, exactly, and go into
 // v_mfma_f32_16x16x32_bf16. Both sum in fp32.
 //
-// The order in which a product takes its contraction elements is free as long as both operands agree, and it
-// is chosen such that each lane's part of a step lies together: with Q = DK / 4 elements of a step for
-// each of the four lane groups, group g takes elements Q g .. Q g + Q - 1, slice after slice. A lane's codes of a
-// step are then Q / 2 consecutive bytes, and its scales Q / 32 consecutive ones.
+// The order in which a product takes its contraction elements is free as long as both operands agree; each
+// kernel takes the one that gives it whole pieces of memory and few reads of LDS.
 #include "mxfp4.h"
 #include "mxfp4_internal.h"
 #include "product_tiles.h"
@@ -27,30 +25,34 @@ struct MxProductArgs {
   uint8_t* out_scales;                    // h in MXFP4
 };
 
-// Chunk c of 16 bytes of a row of CPR chunks sits at c ^ x(row), so that the 16 rows that a fragment read
-// meets (one chunk of each) fall on distinct banks.
-template <int CPR>
-__device__ __forceinline__ int swizzle(int row) {
-  static_assert(CPR == 2 || CPR == 4 || CPR == 8 || CPR == 16 || CPR == 32, "row width");
-  if constexpr (CPR == 2) return row >> 3 & 1;
-  else if constexpr (CPR == 4) return row >> 2 & 3;
-  else if constexpr (CPR == 8) return row >> 1 & 7;
-  else return row & 15;
+// Chunk c of 16 bytes of a row of CPR chunks sits at c ^ x(row), so that the lanes that read LDS together fall on distinct banks.
+// They are, of a fragment read, 8 rows of lane group 0 and the 8 others of group 1 (or of groups 2 and 3). Where the groups
+// read chunks 2^ROT apart, their bits are turned left by ROT from what groups that read neighbouring chunks need. (Without
+// that, 17% of the cycles of the product of 4-bit rows were bank conflicts.)
+template <int CPR, int ROT>
+__device__ __forceinline__ constexpr int swizzle(int row) {
+  static_assert(CPR == 8 || CPR == 32, "row width");
+  constexpr int bits = CPR == 8 ? 3 : 4, all = (1 << bits) - 1;
+  const int x = (CPR == 8 ? row >> 1 : row) & all;
+  return (x << ROT | x >> (bits - ROT)) & all;
 }
 
 // One operand of a tile: T rows of ROWB bytes per step, loaded by NW waves with buffer loads of 1 KB into LDS. PAIR:
-// units of U rows of two matrices in turn (gate, up, gate, ..).
-template <int T, int ROWB, int NW, bool PAIR>
+// units of U rows of two matrices in turn (gate, up, gate, ..). Lane groups read chunks 2^ROT apart.
+template <int T, int ROWB, int NW, int ROT, bool PAIR>
 struct Tile {
-  static constexpr int CPR = ROWB / 16, kChunks = T * CPR, kLoads = kChunks / 64 / NW, kRowsPerLoad = 64 / CPR;
+  static constexpr int CPR = ROWB / 16, kChunks = T * CPR, kAll = kChunks / 64, kRowsPerLoad = 64 / CPR;
+  static constexpr int kLoads = (kAll + NW - 1) / NW, kLeast = kAll / NW;  // of a wave, at most and at least
   static constexpr int U = kRowsPerLoad > 16 ? kRowsPerLoad : 16;
-  static_assert(kLoads >= 1 && kLoads * 64 * NW == kChunks, "loads split evenly over the waves");
-  static_assert(kRowsPerLoad * NW % 16 == 0, "the permutation repeats from one load to the next");
+  static_assert(kAll * 64 == kChunks, "whole loads");
+  // The permutation repeats after this many of a wave's loads.
+  static constexpr int kTurn = CPR < 16 || kRowsPerLoad * NW >= 16 ? 1 : 16 / (kRowsPerLoad * NW);
+  static_assert(CPR >= 16 || kRowsPerLoad * NW % 16 == 0, "the permutation repeats from one load to the next");
   static_assert(!PAIR || T % (2 * U) == 0, "whole pairs of units");
   static constexpr int kOutside = 0x40000000;  // past any extent (at most 256 rows of 2^21 bytes)
 
   const char *base, *base2;
-  int extent, ld, lane_at, at_in_row;
+  int extent, ld, row_at, at_in_row;
 
   // first, count: the tile's first row in the matrix (PAIR: in each of the two) and how many exist
   __device__ __forceinline__ void set(const void* origin, const void* origin2, size_t first, int count, int row_bytes,
@@ -60,26 +62,34 @@ struct Tile {
     base2 = static_cast<const char*>(origin2) + first * row_bytes;
     extent = count * row_bytes;
     const int row = lane / CPR, pos = lane % CPR;
-    at_in_row = (pos ^ swizzle<CPR>(wave * kRowsPerLoad + row)) * 16;
-    lane_at = row * row_bytes + at_in_row;
+    at_in_row = (pos ^ swizzle<CPR, ROT>(wave * kRowsPerLoad + row)) * 16;
+    row_at = row * row_bytes;
   }
   // bytes byte0 .. byte0 + ROWB - 1 of each row into `slot`; past the end of a row (`left` bytes from byte0 on) and
   // in rows that do not exist zeros
-  template <int AUX>
-  __device__ __forceinline__ void issue(u32x4* slot, int byte0, int left, int wave) const {
-    const int at = at_in_row < left ? lane_at : kOutside;
+  // (of PARTS parts of the loads the one given).
+  template <int AUX, int PARTS = 1>
+  __device__ __forceinline__ void issue(u32x4* slot, int byte0, int left, int wave, int part = 0) const {
+    int at[kTurn];
+#pragma unroll
+    for (int i = 0; i < kTurn; ++i) {
+      const int in_row = at_in_row ^ (kTurn > 1 ? swizzle<CPR, ROT>(i * kRowsPerLoad * NW) * 16 : 0);
+      at[i] = in_row < left ? row_at + in_row : kOutside;
+    }
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
+      if (PARTS > 1 && i * PARTS / kLoads != part) continue;
       const int l = wave + i * NW, r0 = l * kRowsPerLoad;
+      if (kLeast < kLoads && l >= kAll) continue;
       const int row0 = PAIR ? (r0 / (2 * U)) * U + r0 % U : r0;
       const char* b = PAIR && (r0 / U & 1) ? base2 : base;
       const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)b, (short)0, extent, kBufferWord3);
-      buffer_load_lds16<AUX>(r, slot + l * 64, at + row0 * ld, byte0);
+      buffer_load_lds16<AUX>(r, slot + l * 64, at[i % kTurn] + row0 * ld, byte0);
     }
   }
   // 16 bytes: chunk c of row m of the slot
   __device__ __forceinline__ static u32x4 read(const u32x4* slot, int m, int c) {
-    return slot[m * CPR + (c ^ swizzle<CPR>(m))];
+    return slot[m * CPR + (c ^ swizzle<CPR, ROT>(m))];
   }
 };
 
@@ -95,11 +105,49 @@ __device__ __forceinline__ void issue_scales(const uint8_t* from, int count, cha
   buffer_load_lds4(r, area + load * 256, load * 256 + lane * 4);
 }
 
-// h = silu(g) u; far results as in swiglu.h
-__device__ __forceinline__ float silu_times(float g, float u) {
-  float h = g * sigmoid<__bf16>(g) * u;
-  if (g < kFar) h = (float)(g * far_sigmoid<__bf16>(g) * u);
-  return h;
+// h = silu(g) u, in place of the gates; far results as in swiglu.h
+template <int N>
+__device__ __forceinline__ void silu_times(float (&g)[N], const float (&u)[N]) {
+  float low = g[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) low = fminf(low, g[i]);  // (NaN is passed over: it needs no care)
+  const bool far = low < kFar;
+  float h[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) h[i] = g[i] * sigmoid<__bf16>(g[i]) * u[i];
+  if (far) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (g[i] < kFar) h[i] = (float)(g[i] * far_sigmoid<__bf16>(g[i]) * u[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) g[i] = h[i];
+}
+template <int NH>
+__device__ __forceinline__ void silu_times(f32x4 (&g)[NH], const f32x4 (&u)[NH]) {
+  float x[4 * NH], y[4 * NH];
+#pragma unroll
+  for (int i = 0; i < 4 * NH; ++i) {
+    x[i] = g[i / 4][i % 4];
+    y[i] = u[i / 4][i % 4];
+  }
+  silu_times(x, y);
+#pragma unroll
+  for (int i = 0; i < 4 * NH; ++i) g[i / 4][i % 4] = x[i];
+}
+
+// 16 rows of h in bf16 from r0 and 32 columns from c0 of the tile, 64 bytes of a row together (store_fragments would write 32).
+__device__ __forceinline__ void store_32_columns(const OutTile& o, bool stream, const f32x4 (&v)[2], int r0, int c0, int lane) {
+  u32x4 q;  // 8 columns of fragment 0 (even lane groups) or 1 (odd ones)
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const auto s = __builtin_amdgcn_permlane16_swap(pack_bf16(v[0][2 * h], v[0][2 * h + 1]),
+                                                    pack_bf16(v[1][2 * h], v[1][2 * h + 1]), false, false);
+    q[h] = s[0];
+    q[2 + h] = s[1];
+  }
+  const int g = lane >> 4;
+  o.put(q, o.at(r0 + (lane & 15), c0 + (g & 1) * 16 + (g >> 1) * 8, 2), stream);
 }
 
 // 16 rows of h from r0 and NH * 16 columns from c0 of the tile, as groups of 32 in MXFP4. v as in store_fragments.
@@ -142,27 +190,43 @@ __device__ __forceinline__ void store_mxfp4(const MxProductArgs& a, const TileAt
   }
 }
 
-// A workgroup of WGM x WGN waves computes a tile of C, each wave WM x WN of it; steps of DK contraction elements go
-// through a ring of RING slots in LDS, the scales of a block of 256 elements through a ring of their own. X4: rows in
-// MXFP4. PAIR: the tile's columns are those of two matrices, U of the one and U of the other in turn, so that a wave
-// holds gate and up of the same columns of h.
-template <bool X4, bool PAIR, int WM, int WN, int WGM, int WGN, int DK, int RING, bool ONCE, bool DEAL>
+// 16 rows of h from r0 and NH * 16 columns from c0 of the tile, in the output's format.
+template <int NH>
+__device__ __forceinline__ void store_h(const MxProductArgs& a, const TileAt& t, const OutTile& o, const f32x4 (&h)[NH], int r0,
+                                        int c0, int lane) {
+  if constexpr (NH % 2 == 0) {
+    if (a.out_scales) return store_mxfp4<NH>(a, t, h, r0, c0, lane);
+  }
+  if constexpr (NH == 2) store_32_columns(o, a.p.stream, h, r0, c0, lane);
+  else store_fragments<NH>(o, a.p, h, r0, c0, lane);
+}
+
+// A workgroup of WGM x WGN waves computes a tile of C, each wave WM x WN of it. Rows go through a ring of RING slots of DK
+// contraction elements in LDS. Codes and their scales go through a ring of blocks of 256 elements, so that a load takes whole
+// lines of a row: X4 (rows in MXFP4) has steps of a block, as many slots as the rows and both operands loaded
+// together; bf16 rows have four steps to a block and two blocks, the next of which is loaded in four parts. PAIR: the
+// tile's columns are those of two matrices, 16 of the one and 16 of the other in turn, so that a wave holds gate and up of
+// the same columns of h.
+template <bool X4, bool PAIR, int WM, int WN, int WGM, int WGN, int RING, bool DEAL>
 __global__ __launch_bounds__(64 * WGM * WGN) void mx_kernel(MxProductArgs a) {
   constexpr int TM = WM * WGM, TN = WN * WGN, NW = WGM * WGN;
   constexpr int MF = WM / 16, NF = WN / 16;
-  constexpr int NS = DK / (X4 ? 128 : 32);  // slices of a step: one matrix instruction per pair of fragments
-  constexpr int Q = DK / 4;                 // elements of a step per lane group
-  using OA = Tile<TM, X4 ? DK / 2 : DK * 2, NW, false>;
-  using OB = Tile<TN, DK / 2, NW, PAIR>;
-  constexpr int STAGE = OA::kChunks + OB::kChunks, LOADS = OA::kLoads + OB::kLoads;
-  constexpr int SPB = kMxBlock / DK;        // steps per block of scales
-  constexpr int SR = (RING + SPB - 2) / SPB + 1;  // blocks that RING steps in a row may meet
+  constexpr int DK = X4 ? kMxBlock : 64;
+  constexpr int NS = 2;                     // slices of a step: one matrix instruction per pair of fragments
+  using OA = Tile<TM, 128, NW, 1, false>;
+  using OB = Tile<TN, 128, NW, 1, PAIR>;
+  constexpr int SPB = kMxBlock / DK;        // steps per block
+  constexpr int RB = X4 ? RING : 2;         // blocks in LDS
+  constexpr int LOADS = OA::kLeast + (X4 ? OB::kLeast : 0);
   constexpr int LA = X4 ? scale_loads(TM) : 0, LB = scale_loads(PAIR ? TN / 2 : TN), LT = LA + LB * (PAIR ? 2 : 1);
-  static_assert(DK <= kMxBlock && (!X4 || DK == kMxBlock), "steps within a block");
+  static_assert(X4 || RING == 2, "the parts of a block are timed for two slots");
   static_assert(!PAIR || WN % (2 * OB::U) == 0, "a wave holds whole pairs");
-  static_assert((RING * STAGE * 16 + SR * LT * 256) <= 160 * 1024, "LDS");
-  __shared__ __align__(16) u32x4 ring[RING * STAGE];
-  __shared__ __align__(16) char scale_ring[SR * LT * 256];
+  static_assert(RING * OA::kChunks * 16 + RB * (OB::kChunks * 16 + LT * 256) <= 160 * 1024, "LDS");
+  // (One object: with several, the compiler takes reads of each to depend on the loads into it that are in flight and waits for
+  // all of them first. What is read has landed, the kernel's own waits see to that.)
+  __shared__ __align__(16) u32x4 ring[RING * OA::kChunks + RB * (OB::kChunks + LT * 16)];
+  u32x4* const code_ring = ring + RING * OA::kChunks;
+  char* const scale_ring = reinterpret_cast<char*>(code_ring + RB * OB::kChunks);
   const ProductArgs& p = a.p;
   TileAt t;
   if (!tile_at<kForward, DEAL>(p, TM, PAIR ? TN / 2 : TN, t)) return;
@@ -179,14 +243,10 @@ __global__ __launch_bounds__(64 * WGM * WGN) void mx_kernel(MxProductArgs a) {
   const size_t we = (size_t)t.e * p.N * (K / 2);
   ob.set(static_cast<const char*>(p.b) + we, PAIR ? static_cast<const char*>(p.b2) + we : nullptr, t.c0, t.clim, K / 2,
          wave, lane);
-  // The expert's weights are read by this row tile alone, in whole lines.
-  const bool once = ONCE && DK == kMxBlock && t.rb - t.ra <= TM && K % kMxBlock == 0;
 
-  auto issue = [&](int st) __attribute__((always_inline)) {
-    // A block's scales go before the first step that uses them: whoever waits for that step's operands has them too.
-    if (SPB == 1 || st % SPB == 0) {
-      const int b = st / SPB;
-      char* area = scale_ring + b % SR * (LT * 256);
+  auto issue_block = [&](int b, int part) __attribute__((always_inline)) {
+    if (part == 0) {
+      char* area = scale_ring + b % RB * (LT * 256);
       const size_t wb = mx_scale_at(t.e, blocks, b, p.N, t.c0);
 #pragma unroll
       for (int i = 0; i < (LT + NW - 1) / NW; ++i) {
@@ -196,19 +256,27 @@ __global__ __launch_bounds__(64 * WGM * WGN) void mx_kernel(MxProductArgs a) {
         else if (PAIR && l < LT) issue_scales(a.b2_scales + wb, t.clim, area + (LA + LB) * 256, l - LA - LB, lane);
       }
     }
-    u32x4* slot = ring + st % RING * STAGE;
-    const int k0 = st * DK;
-    oa.template issue<0>(slot, X4 ? k0 / 2 : k0 * 2, a_bytes - (X4 ? k0 / 2 : k0 * 2), wave);
-    if (once) ob.template issue<kNonTemporal>(slot + OA::kChunks, k0 / 2, (K - k0) / 2, wave);
-    else ob.template issue<0>(slot + OA::kChunks, k0 / 2, (K - k0) / 2, wave);
+    ob.template issue<0, SPB>(code_ring + b % RB * OB::kChunks, b * 128, K / 2 - b * 128, wave, part);
   };
-  // Scales of this lane's groups of step st: byte i for its i-th group. Groups past K hold zeros under whatever their scale
-  // bytes are; their scale is taken to be 2^-127, so that zeros they stay.
+  // Rows of step st, and the codes whose turn it is: X4 those of the step; else, once all are done with block q - 1 (the
+  // barrier in step 4q - 1, when the rows of step 4q + 1 are issued), one part of block q + 1 with each of steps
+  // 4q + 1 .. 4q + 4. Codes go before the rows: whoever waits for step 4q + 4's rows has block q + 1 too.
+  auto issue = [&](int st) __attribute__((always_inline)) {
+    if constexpr (X4) {
+      issue_block(st, 0);
+    } else {
+      const int at = st - 1;
+      if (at >= 0 && at / SPB + 1 < blocks) issue_block(at / SPB + 1, at % SPB);
+    }
+    oa.template issue<0>(ring + st % RING * OA::kChunks, st * 128, a_bytes - st * 128, wave);
+  };
+  // Scales of this lane's groups of step st: X4 two, in two bytes; else one. Groups past K hold zeros under whatever their
+  // scale bytes are; their scale is taken to be 2^-127, so that zeros they stay.
   const int groups = K / kMxGroup;
   auto scales_of = [&](const char* rows, int m, int st) __attribute__((always_inline)) {
-    const int first = st * (DK / kMxGroup) + (DK >= 128 ? lg * (Q / 32) : lg / 2);  // group of the whole row
+    const int first = st * (DK / kMxGroup) + (X4 ? lg * 2 : lg / 2);  // group of the whole row
     const char* at = rows + (m + lr) * 8 + (first & 7);
-    if constexpr (DK == 256) {
+    if constexpr (X4) {
       const unsigned s = *reinterpret_cast<const unsigned short*>(at);
       return first + 1 < groups ? s : (first < groups ? s & 0xffu : 0u);
     } else {
@@ -217,17 +285,13 @@ __global__ __launch_bounds__(64 * WGM * WGN) void mx_kernel(MxProductArgs a) {
     }
   };
   auto a_scales = [&](int st, int i) __attribute__((always_inline)) {
-    return scales_of(scale_ring + st / SPB % SR * (LT * 256), wm + i * 16, st);
+    return scales_of(scale_ring + st / SPB % RB * (LT * 256), wm + i * 16, st);
   };
   auto b_scales = [&](int st, int j) __attribute__((always_inline)) {
-    const char* area = scale_ring + st / SPB % SR * (LT * 256) + LA * 256;
+    const char* area = scale_ring + st / SPB % RB * (LT * 256) + LA * 256;
     const int n = wn + j * 16;
-    if constexpr (PAIR) {
-      constexpr int U = OB::U;
-      return scales_of(area + (n / U & 1) * (LB * 256), n / (2 * U) * U + n % U, st);
-    } else {
-      return scales_of(area, n, st);
-    }
+    if constexpr (PAIR) return scales_of(area + (n / 16 & 1) * (LB * 256), n / 32 * 16, st);
+    else return scales_of(area, n, st);
   };
 
   auto run = [&](auto present) __attribute__((always_inline)) {
@@ -237,47 +301,63 @@ __global__ __launch_bounds__(64 * WGM * WGN) void mx_kernel(MxProductArgs a) {
     for (int i = 0; i < F; ++i)
 #pragma unroll
       for (int j = 0; j < NF; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    u32x4 fa[F ? F : 1];
-    unsigned sa[F ? F : 1], sb[NF], sn[NF];  // sn: the next step's
-    u32x4 fb[2][NF];  // X4: codes; else bf16 values
+    u32x4 fa[F ? F : 1], fb[2][NF];   // fb: codes (X4) or bf16 values
+    unsigned sa[F ? F : 1], sb[NF], sn[NF];  // scales; sn: the next step's
+    u32x2 codes[NF];                  // of a step's two slices (bf16 rows)
     auto read_a = [&](const u32x4* slot, int i, int h) __attribute__((always_inline)) {
       return OA::read(slot, wm + i * 16 + lr, lg * NS + h);
     };
-    // B's fragment of slice h: the codes of 32 elements (X4), or 8 elements converted
-    auto read_b = [&](const u32x4* slot, int j, int h, unsigned scale) __attribute__((always_inline)) {
+    // The codes of step st, 16 bytes for slice h (X4) or 8 for both slices.
+    auto read_codes = [&](int st, int j, int h) __attribute__((always_inline)) {
+      const u32x4* slot = code_ring + st / SPB % RB * OB::kChunks;
       const int n = wn + j * 16 + lr;
       if constexpr (X4) {
-        return OB::read(slot + OA::kChunks, n, lg * NS + h);
+        return OB::read(slot, n, lg * NS + h);
       } else {
-        const int byte = lg * (Q / 2) + h * 4, c = byte / 16;
-        const unsigned* at = reinterpret_cast<const unsigned*>(slot + OA::kChunks + n * OB::CPR + (c ^ swizzle<OB::CPR>(n)));
-        const unsigned s = DK == 256 ? (h < NS / 2 ? scale & 0xffu : scale >> 8) : scale;
-        return __builtin_bit_cast(u32x4, mx_bf16x8(at[byte / 4 % 4], mx_scale_f32(s)));
+        const int c = (st % SPB * 2 + (lg >> 1)) ^ swizzle<8, 1>(n);
+        return reinterpret_cast<const u32x2*>(slot)[(n * 8 + c) * 2 + (lg & 1)];
       }
     };
-    if (steps > 0) {
+    auto convert = [&](int j, int h, unsigned scale) __attribute__((always_inline)) {
+      return __builtin_bit_cast(u32x4, mx_bf16x8(codes[j][h], mx_scale_f32(scale)));
+    };
+    for (int i = 0; i < (X4 ? 0 : SPB); ++i) issue_block(0, i);
 #pragma unroll
-      for (int r = 0; r < RING; ++r)
-        if (r < steps) issue(r);
-      wait_steps<LOADS, RING - 1>(steps - 1);
-      bare_barrier();
-#pragma unroll
-      for (int j = 0; j < (F ? NF : 0); ++j) {
-        sb[j] = b_scales(0, j);
-        fb[0][j] = read_b(ring, j, 0, sb[j]);
+    for (int r = 0; r < RING; ++r)
+      if (r < steps) issue(r);
+    wait_steps<LOADS, RING - 1>(steps - 1);
+    bare_barrier();
+    auto product = [&](int i, int j, u32x4 x, auto hc) __attribute__((always_inline)) {
+      constexpr int h = decltype(hc)::value;
+      if constexpr (X4) {
+        const u32x4 y = fa[i];
+        const i32x8 w{(int)x[0], (int)x[1], (int)x[2], (int)x[3], 0, 0, 0, 0};
+        const i32x8 v{(int)y[0], (int)y[1], (int)y[2], (int)y[3], 0, 0, 0, 0};
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, v, acc[i][j], 4, 4, h, (int)sb[j], h, (int)sa[i]);
+      } else {
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, fa[i]),
+                                                            acc[i][j], 0, 0, 0);
       }
+    };
 #pragma unroll
-      for (int i = 0; i < F; ++i) {
-        if (X4) sa[i] = a_scales(0, i);
-        fa[i] = read_a(ring, i, 0);
+    for (int j = 0; j < (F ? NF : 0); ++j) {
+      sb[j] = b_scales(0, j);
+      if constexpr (X4) fb[0][j] = read_codes(0, j, 0);
+      else {
+        codes[j] = read_codes(0, j, 0);
+        fb[0][j] = convert(j, 0, sb[j]);
       }
     }
+#pragma unroll
+    for (int i = 0; i < F; ++i) {
+      if (X4) sa[i] = a_scales(0, i);
+      fa[i] = read_a(ring, i, 0);
+    }
     for (int st = 0; st < steps; ++st) {
-      const u32x4* slot = ring + st % RING * STAGE;
-      const u32x4* next = ring + (st + 1) % RING * STAGE;
+      const u32x4* slot = ring + st % RING * OA::kChunks;
+      const u32x4* next = ring + (st + 1) % RING * OA::kChunks;
       static_for<NS>([&](auto hc) __attribute__((always_inline)) {
         constexpr int h = decltype(hc)::value, cur = h & 1;
-        static_assert(NS % 2 == 0, "fragments alternate");
         constexpr bool last = h == NS - 1;
         if (last) {
           wait_lgkmcnt0();  // this wave's reads of step st are back
@@ -294,25 +374,29 @@ __global__ __launch_bounds__(64 * WGM * WGN) void mx_kernel(MxProductArgs a) {
 #pragma unroll
         for (int j = 0; j < (F ? NF : 0); ++j) {
           if (last) sn[j] = b_scales(st + 1, j);
-          fb[cur ^ 1][j] = read_b(rs, j, rh, last ? sn[j] : sb[j]);
+          if constexpr (X4) fb[cur ^ 1][j] = read_codes(st + last, j, rh);
+          else if (last) codes[j] = read_codes(st + 1, j, 0);
         }
 #pragma unroll
         for (int i = 0; i < F; ++i) {
+          if (!X4 && i == F / 2) {  // the codes have had time to arrive
 #pragma unroll
-          for (int j = 0; j < NF; ++j) {
-            if constexpr (X4) {
-              const u32x4 x = fb[cur][j], y = fa[i];
-              const i32x8 w{(int)x[0], (int)x[1], (int)x[2], (int)x[3], 0, 0, 0, 0};
-              const i32x8 v{(int)y[0], (int)y[1], (int)y[2], (int)y[3], 0, 0, 0, 0};
-              acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, v, acc[i][j], 4, 4, h, (int)sb[j], h,
-                                                                          (int)sa[i]);
-            } else {
-              acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, fb[cur][j]),
-                                                                  __builtin_bit_cast(bf16x8, fa[i]), acc[i][j], 0, 0, 0);
-            }
+            for (int j = 0; j < NF; ++j) fb[cur ^ 1][j] = convert(j, rh, last ? sn[j] : sb[j]);
           }
+#pragma unroll
+          for (int j = 0; j < NF; ++j) product(i, j, fb[cur][j], hc);
           fa[i] = read_a(rs, i, rh);
           if (X4 && last) sa[i] = a_scales(st + 1, i);
+        }
+        // order of the slice for bf16 rows: the reads of codes and scales, then each row fragment's products and its next read
+        // (65,536 rows over 32 experts of 2048 x 7168: 1,452 us against 1,479; with 4-bit rows 547 against 537)
+        if constexpr (!X4 && F > 0) {
+          if (last) __builtin_amdgcn_sched_group_barrier(0x100, 2 * NF, 0);
+#pragma unroll
+          for (int i = 0; i < F; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, NF, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+          }
         }
         __atomic_signal_fence(__ATOMIC_SEQ_CST);  // the reads stay in this slice
       });
@@ -320,29 +404,21 @@ __global__ __launch_bounds__(64 * WGM * WGN) void mx_kernel(MxProductArgs a) {
       for (int j = 0; j < NF; ++j) sb[j] = sn[j];
     }
     OutTile o;
+    o.set(p, row0, t.mlim, t.c0, t.clim, p.N);
     if constexpr (PAIR) {
-      constexpr int UF = OB::U / 16, NH = NF / 2;
-      o.set(p, row0, t.mlim, t.c0, t.clim, p.N);
+      constexpr int NH = NF / 2;
 #pragma unroll
       for (int i = 0; i < F; ++i) {
-        f32x4 h[NH];
+        f32x4 h[NH], u[NH];
 #pragma unroll
-        for (int q = 0; q < NH; ++q)
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            constexpr int two = 2 * UF;
-            h[q][x] = silu_times(acc[i][q / UF * two + q % UF][x], acc[i][q / UF * two + q % UF + UF][x]);
-          }
-        if constexpr (NH % 2 == 0) {
-          if (a.out_scales) {
-            store_mxfp4<NH>(a, t, h, wm + i * 16, wn / 2, lane);
-            continue;
-          }
+        for (int q = 0; q < NH; ++q) {
+          h[q] = acc[i][2 * q];
+          u[q] = acc[i][2 * q + 1];
         }
-        store_fragments<NH>(o, p, h, wm + i * 16, wn / 2, lane);
+        silu_times(h, u);
+        store_h<NH>(a, t, o, h, wm + i * 16, wn / 2, lane);
       }
     } else {
-      o.set(p, row0, t.mlim, t.c0, t.clim, p.N);
 #pragma unroll
       for (int i = 0; i < F; ++i) store_fragments<NF>(o, p, acc[i], wm + i * 16, wn, lane);
     }
@@ -357,11 +433,448 @@ __global__ __launch_bounds__(64 * WGM * WGN) void mx_kernel(MxProductArgs a) {
   }
 }
 
-template <bool X4, bool PAIR, int WM, int WN, int WGM, int WGN, int DK, int RING, bool ONCE, bool DEAL>
+// Few rows per expert: the weights' codes go straight to registers, DEPTH - 1 blocks of 256 contraction elements ahead, the
+// rows, which all waves share, through a ring of DEPTH slots in LDS. A wave takes MF * 16 rows and NF * 16 columns (PAIR: NF / 2
+// fragments of gate and as many of up), the NW waves of a workgroup neighbouring columns. Of each half of a block (128
+// elements) a lane holds one group of 32 of each of its weight rows, so that a load takes 64 bytes of 16 rows.
+template <bool X4, bool PAIR, int MF, int NF, int NW, int DEPTH>
+__global__ __launch_bounds__(64 * NW) void mx_rows_kernel(MxProductArgs a) {
+  constexpr int TM = 16 * MF, WN = 16 * NF, TN = WN * NW, TH = PAIR ? TN / 2 : TN, WH = PAIR ? WN / 2 : WN;
+  constexpr int NH = PAIR ? NF / 2 : NF, kRowBytes = X4 ? 128 : 512;
+  using OA = Tile<TM, kRowBytes, NW, X4 ? 0 : 2, false>;
+  constexpr int LA = X4 ? scale_loads(TM) : 0;
+  constexpr int kOutside = 0x40000000;
+  // loads of a block by every wave: rows, codes and scales (those that only some waves make just lengthen their waits)
+  constexpr int LOADS = OA::kLeast + 3 * NF;
+  __shared__ __align__(16) u32x4 ring[DEPTH * (OA::kChunks + LA * 16)];  // (one object: see mx_kernel)
+  char* const scale_ring = reinterpret_cast<char*>(ring + DEPTH * OA::kChunks);
+  const ProductArgs& p = a.p;
+  TileAt t;
+  if (!tile_at<kForward, false>(p, TM, TH, t)) return;
+  const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int K = p.K, blocks = mx_blocks(K), ld = K / 2, a_ld = X4 ? ld : K * 2, groups = K / kMxGroup;
+  const size_t row0 = (size_t)t.ra + t.m0, we = (size_t)t.e * p.N * ld + (size_t)t.c0 * ld;
+  OA oa;
+  oa.set(p.a, p.a, row0, t.mlim, a_ld, wave, lane);
+  const __amdgpu_buffer_rsrc_t rb =
+      __builtin_amdgcn_make_buffer_rsrc((void*)(static_cast<const char*>(p.b) + we), (short)0, t.clim * ld, kBufferWord3);
+  const __amdgpu_buffer_rsrc_t rb2 = __builtin_amdgcn_make_buffer_rsrc(
+      PAIR ? (void*)(static_cast<const char*>(p.b2) + we) : nullptr, (short)0, PAIR ? t.clim * ld : 0, kBufferWord3);
+
+  struct Block {
+    u32x4 b[NF][2];
+    u32x2 s[NF];
+  };
+  // block b (past the last: zeros) into slot i of the ring and into q
+  auto load = [&](Block& q, int b, int i) __attribute__((always_inline)) {
+    const bool in = b < blocks;
+    const int at = b * 128 + lg * 16;  // of the lane's codes in a row
+    oa.template issue<0>(ring + i * OA::kChunks, b * kRowBytes, a_ld - b * kRowBytes, wave);
+    const size_t ws = mx_scale_at(t.e, blocks, in ? b : 0, p.N, t.c0);
+    const __amdgpu_buffer_rsrc_t s =
+        __builtin_amdgcn_make_buffer_rsrc((void*)(a.b_scales + ws), (short)0, in ? t.clim * 8 : 0, kBufferWord3);
+    const __amdgpu_buffer_rsrc_t s2 = __builtin_amdgcn_make_buffer_rsrc(
+        PAIR ? (void*)(a.b2_scales + ws) : nullptr, (short)0, PAIR && in ? t.clim * 8 : 0, kBufferWord3);
+#pragma unroll
+    for (int j = 0; j < NF; ++j) {
+      const bool up = PAIR && j >= NH;
+      const int n = wave * WH + (up ? j - NH : j) * 16 + lr;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        q.b[j][h] = __builtin_amdgcn_raw_buffer_load_b128(up ? rb2 : rb, at + h * 64 < ld ? n * ld + at + h * 64 : kOutside, 0, 0);
+      q.s[j] = __builtin_amdgcn_raw_buffer_load_b64(up ? s2 : s, n * 8, 0, 0);
+    }
+    if (X4 && wave < LA)
+      issue_scales(a.a_scales + mx_scale_at(0, 0, in ? b : 0, p.rows, row0), in ? t.mlim : 0, scale_ring + i * LA * 256, wave,
+                   lane);
+  };
+  auto run = [&](auto present) __attribute__((always_inline)) {
+    constexpr int F = decltype(present)::value;
+    f32x4 acc[F][NF];
+#pragma unroll
+    for (int i = 0; i < F; ++i)
+#pragma unroll
+      for (int j = 0; j < NF; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    auto multiply = [&](const Block& q, int b, int slot) __attribute__((always_inline)) {
+      const u32x4* rows = ring + slot * OA::kChunks;
+      static_for<2>([&](auto hc) __attribute__((always_inline)) {
+        constexpr int h = decltype(hc)::value;
+        // A group past K holds zeros; its scale is taken to be 2^-127 whatever the byte, so that zeros they stay.
+        const unsigned mask = b * 8 + h * 4 + lg < groups ? 0xffu : 0u;
+        unsigned s[NF];
+#pragma unroll
+        for (int j = 0; j < NF; ++j) s[j] = q.s[j][h] >> lg * 8 & mask;
+        if constexpr (X4) {
+#pragma unroll
+          for (int i = 0; i < F; ++i) {
+            const u32x4 y = OA::read(rows, i * 16 + lr, h * 4 + lg);
+            const unsigned sa =
+                *reinterpret_cast<const unsigned char*>(scale_ring + slot * LA * 256 + (i * 16 + lr) * 8 + h * 4 + lg) & mask;
+            const i32x8 v{(int)y[0], (int)y[1], (int)y[2], (int)y[3], 0, 0, 0, 0};
+#pragma unroll
+            for (int j = 0; j < NF; ++j) {
+              const u32x4 x = q.b[j][h];
+              const i32x8 w{(int)x[0], (int)x[1], (int)x[2], (int)x[3], 0, 0, 0, 0};
+              acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, v, acc[i][j], 4, 4, 0, (int)s[j], 0, (int)sa);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            bf16x8 w[NF];
+#pragma unroll
+            for (int j = 0; j < NF; ++j) w[j] = mx_bf16x8(q.b[j][h][k], mx_scale_f32(s[j]));
+#pragma unroll
+            for (int i = 0; i < F; ++i) {
+              const bf16x8 v = __builtin_bit_cast(bf16x8, OA::read(rows, i * 16 + lr, h * 16 + lg * 4 + k));
+#pragma unroll
+              for (int j = 0; j < NF; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[j], v, acc[i][j], 0, 0, 0);
+            }
+          }
+        }
+      });
+    };
+    Block q[DEPTH];
+#pragma unroll
+    for (int i = 0; i < DEPTH - 1; ++i) load(q[i], i, i);
+    for (int b0 = 0; b0 < blocks; b0 += DEPTH) {
+      static_for<DEPTH>([&](auto ic) __attribute__((always_inline)) {
+        constexpr int i = decltype(ic)::value;
+        const int b = b0 + i;
+        if (b < blocks) {
+          wait_vmcnt<(DEPTH - 2) * LOADS>();  // block b has landed for this wave, and after the barrier for all;
+          wait_lgkmcnt0();
+          bare_barrier();                     // all are done with block b - 1
+          load(q[(i + DEPTH - 1) % DEPTH], b + DEPTH - 1, (i + DEPTH - 1) % DEPTH);
+          multiply(q[i], b, i);
+          __atomic_signal_fence(__ATOMIC_SEQ_CST);
+        }
+      });
+    }
+    OutTile o;
+    o.set(p, row0, t.mlim, t.c0, t.clim, p.N);
+#pragma unroll
+    for (int i = 0; i < F; ++i) {
+      if constexpr (PAIR) {
+        f32x4 h[NH], u[NH];
+#pragma unroll
+        for (int j = 0; j < NH; ++j) {
+          h[j] = acc[i][j];
+          u[j] = acc[i][j + NH];
+        }
+        silu_times(h, u);
+        store_h<NH>(a, t, o, h, i * 16, wave * WH, lane);
+      } else {
+        store_fragments<NF>(o, p, acc[i], i * 16, wave * WN, lane);
+      }
+    }
+  };
+  const int mine = __builtin_amdgcn_readfirstlane((t.mlim + 15) / 16);
+  static_for<MF>([&](auto c) __attribute__((always_inline)) {
+    if (mine == decltype(c)::value + 1) run(std::integral_constant<int, decltype(c)::value + 1>{});
+  });
+}
+
+// Few rows and few tiles: no LDS on the operands' way. A workgroup takes 16 rows and NF * 16 columns (PAIR: NF / 2 fragments of
+// gate and as many of up), and its NW waves share the contraction, wave w blocks w, w + NW, .. of 256 elements, in
+// the order of mx_rows_kernel. Blocks are loaded DEPTH ahead; at the end the waves' sums are joined in order in LDS.
+template <bool X4, bool PAIR, int NF, int NW, int DEPTH>
+__global__ __launch_bounds__(64 * NW) void mx_stream_kernel(MxProductArgs a) {
+  constexpr int TN = 16 * NF, TH = PAIR ? TN / 2 : TN, kThreads = 64 * NW, NH = PAIR ? NF / 2 : NF;
+  constexpr int kPitch = TN + 4;
+  constexpr int kOutside = 0x40000000;
+  __shared__ __align__(16) float sums[NW][16][kPitch];
+  const ProductArgs& p = a.p;
+  TileAt t;
+  if (!tile_at<kForward, false>(p, 16, TH, t)) return;
+  const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int K = p.K, blocks = mx_blocks(K), ld = K / 2, a_ld = X4 ? ld : K * 2, groups = K / kMxGroup;
+  const size_t row0 = (size_t)t.ra + t.m0, we = (size_t)t.e * p.N * ld + (size_t)t.c0 * ld;
+  const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
+      (void*)(static_cast<const char*>(p.a) + row0 * a_ld), (short)0, t.mlim * a_ld, kBufferWord3);
+  const __amdgpu_buffer_rsrc_t rb =
+      __builtin_amdgcn_make_buffer_rsrc((void*)(static_cast<const char*>(p.b) + we), (short)0, t.clim * ld, kBufferWord3);
+  const __amdgpu_buffer_rsrc_t rb2 = __builtin_amdgcn_make_buffer_rsrc(
+      PAIR ? (void*)(static_cast<const char*>(p.b2) + we) : nullptr, (short)0, PAIR ? t.clim * ld : 0, kBufferWord3);
+
+  struct Block {
+    u32x4 a[X4 ? 2 : 8], b[NF][2];
+    u32x2 sa, sb[NF];
+  };
+  auto load = [&](Block& q, int b) __attribute__((always_inline)) {
+    const bool in = b < blocks;
+    const int at = b * 128 + lg * 16;  // of the lane's codes in a row
+    const size_t ws = mx_scale_at(t.e, blocks, in ? b : 0, p.N, t.c0);
+    const __amdgpu_buffer_rsrc_t s =
+        __builtin_amdgcn_make_buffer_rsrc((void*)(a.b_scales + ws), (short)0, in ? t.clim * 8 : 0, kBufferWord3);
+    const __amdgpu_buffer_rsrc_t s2 = __builtin_amdgcn_make_buffer_rsrc(
+        PAIR ? (void*)(a.b2_scales + ws) : nullptr, (short)0, PAIR && in ? t.clim * 8 : 0, kBufferWord3);
+#pragma unroll
+    for (int j = 0; j < NF; ++j) {
+      const bool up = PAIR && j >= NH;
+      const int n = (up ? j - NH : j) * 16 + lr;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        q.b[j][h] = __builtin_amdgcn_raw_buffer_load_b128(up ? rb2 : rb, at + h * 64 < ld ? n * ld + at + h * 64 : kOutside, 0, 0);
+      q.sb[j] = __builtin_amdgcn_raw_buffer_load_b64(up ? s2 : s, n * 8, 0, 0);
+    }
+    if constexpr (X4) {
+      const __amdgpu_buffer_rsrc_t sa = __builtin_amdgcn_make_buffer_rsrc(
+          (void*)(a.a_scales + mx_scale_at(0, 0, in ? b : 0, p.rows, row0)), (short)0, in ? t.mlim * 8 : 0, kBufferWord3);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        q.a[h] = __builtin_amdgcn_raw_buffer_load_b128(ra, at + h * 64 < ld ? lr * ld + at + h * 64 : kOutside, 0, 0);
+      q.sa = __builtin_amdgcn_raw_buffer_load_b64(sa, lr * 8, 0, 0);
+    } else {
+#pragma unroll
+      for (int h = 0; h < 8; ++h)
+        q.a[h] = __builtin_amdgcn_raw_buffer_load_b128(
+            ra, at + h / 4 * 64 < ld ? lr * a_ld + (at + h / 4 * 64) * 4 + h % 4 * 16 : kOutside, 0, 0);
+    }
+  };
+  f32x4 acc[NF];
+#pragma unroll
+  for (int j = 0; j < NF; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  // A group past K holds zeros; its scale is taken to be 2^-127 whatever the byte, so that zeros they stay.
+  auto multiply = [&](const Block& q, int b) __attribute__((always_inline)) {
+    static_for<2>([&](auto hc) __attribute__((always_inline)) {
+      constexpr int h = decltype(hc)::value;
+      const unsigned mask = b * 8 + h * 4 + lg < groups ? 0xffu : 0u;
+      unsigned s[NF];
+#pragma unroll
+      for (int j = 0; j < NF; ++j) s[j] = q.sb[j][h] >> lg * 8 & mask;
+      if constexpr (X4) {
+        const u32x4 y = q.a[h];
+        const i32x8 v{(int)y[0], (int)y[1], (int)y[2], (int)y[3], 0, 0, 0, 0};
+        const unsigned sa = q.sa[h] >> lg * 8 & mask;
+#pragma unroll
+        for (int j = 0; j < NF; ++j) {
+          const u32x4 x = q.b[j][h];
+          const i32x8 w{(int)x[0], (int)x[1], (int)x[2], (int)x[3], 0, 0, 0, 0};
+          acc[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, v, acc[j], 4, 4, 0, (int)s[j], 0, (int)sa);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int j = 0; j < NF; ++j)
+            acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(mx_bf16x8(q.b[j][h][k], mx_scale_f32(s[j])),
+                                                             __builtin_bit_cast(bf16x8, q.a[h * 4 + k]), acc[j], 0, 0, 0);
+      }
+    });
+  };
+  Block q[DEPTH];
+#pragma unroll
+  for (int i = 0; i < DEPTH; ++i) load(q[i], wave + i * NW);
+  for (int b = wave; b < blocks; b += DEPTH * NW) {
+#pragma unroll
+    for (int i = 0; i < DEPTH; ++i) {
+      multiply(q[i], b + i * NW);
+      load(q[i], b + (i + DEPTH) * NW);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < NF; ++j) *reinterpret_cast<f32x4*>(&sums[wave][lr][j * 16 + lg * 4]) = acc[j];
+  __syncthreads();
+  auto sum = [&](int r, int c) __attribute__((always_inline)) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) v += sums[w][r][c];
+    return v;
+  };
+  // a thread takes columns c of rows r, r + kThreads / TH, ..
+  const int c = threadIdx.x % TH;
+#pragma unroll
+  for (int r = threadIdx.x / TH; r < 16; r += kThreads / TH) {
+    float v = sum(r, c);
+    if constexpr (PAIR) {
+      float g[1] = {v};
+      const float u[1] = {sum(r, c + TH)};
+      silu_times(g, u);
+      v = g[0];
+    }
+    const size_t row = row0 + r;
+    const int col = t.c0 + c;
+    const bool in = r < t.mlim && c < t.clim;
+    if constexpr (PAIR && TH % 32 == 0) {
+      if (a.out_scales) {  // 32 threads in a row hold a group
+        unsigned top = __float_as_uint(v) & 0x7fffffffu;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) top = max(top, (unsigned)__shfl_xor((int)top, d));
+        const int scale = mx_scale(top);
+        const float q0 = v * mx_inverse(scale), q1 = __shfl_xor(q0, 1);
+        const unsigned code = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, q0, q1, 1.0f, 0);
+        if (in && !(c & 1))
+          static_cast<uint8_t*>(p.out)[(row * p.N + col) / 2] = scale == kMxNan ? 0 : (uint8_t)code;
+        if (in && !(c & 31))
+          a.out_scales[mx_scale_at(0, 0, col / kMxBlock, p.rows, row) + (col / kMxGroup & 7)] = (uint8_t)scale;
+        continue;
+      }
+    }
+    if (!in) continue;
+    if (p.out_bf16) static_cast<__bf16*>(p.out)[row * p.N + col] = (__bf16)v;
+    else static_cast<float*>(p.out)[row * p.N + col] = v;
+  }
+}
+
+template <bool X4, bool PAIR, int MF, int NF, int NW, int DEPTH>
+hipError_t launch_rows(const MxGemmArgs& a, const MxProductArgs& p, hipStream_t stream) {
+  const long long grid = xcd_grid(tile_items(kForward, a.g, 16 * MF, (PAIR ? 8 : 16) * NF * NW));
+  mx_rows_kernel<X4, PAIR, MF, NF, NW, DEPTH><<<(unsigned)grid, 64 * NW, 0, stream>>>(p);
+  return hipGetLastError();
+}
+
+template <bool X4, bool PAIR, int NF, int NW, int DEPTH>
+hipError_t launch_stream(const MxGemmArgs& a, const MxProductArgs& p, hipStream_t stream) {
+  const long long grid = xcd_grid(tile_items(kForward, a.g, 16, PAIR ? 8 * NF : 16 * NF));
+  mx_stream_kernel<X4, PAIR, NF, NW, DEPTH><<<(unsigned)grid, 64 * NW, 0, stream>>>(p);
+  return hipGetLastError();
+}
+
+template <bool X4, bool PAIR, int WM, int WN, int WGM, int WGN, int RING, bool DEAL>
 hipError_t launch_mx(const MxGemmArgs& a, const MxProductArgs& p, hipStream_t stream) {
   const long long grid = xcd_grid(tile_items(kForward, a.g, WM * WGM, PAIR ? WN * WGN / 2 : WN * WGN));
-  mx_kernel<X4, PAIR, WM, WN, WGM, WGN, DK, RING, ONCE, DEAL><<<(unsigned)grid, 64 * WGM * WGN, 0, stream>>>(p);
+  mx_kernel<X4, PAIR, WM, WN, WGM, WGN, RING, DEAL><<<(unsigned)grid, 64 * WGM * WGN, 0, stream>>>(p);
   return hipGetLastError();
+}
+
+// What a launch may take, and the time of a block of 256 contraction elements (us): `full` for as many tiles of TM x TN (PAIR: TN
+// columns of h) as the CUs work on at a time, `alone` for a last round with at most one to a CU. `start`: what a tile takes before
+// and after its blocks. From products of 1 to 32,768 rows over 1 to 64 experts, of K = 4096, 2048 and 800.
+struct Shape {
+  TileCost cost;
+  double start;
+  bool groups;  // a wave holds groups of 32 columns of h, as h in MXFP4 needs
+};
+template <bool X4, bool PAIR>
+struct Shapes;
+template <>
+struct Shapes<false, false> {
+  static constexpr Shape all[] = {
+      {{16, 32, 1, 0.39, 0.40}, 3.3, false},   // stream: 2 fragments, 8 waves
+      {{16, 64, 1, 0.49, 0.50}, 3.4, false},   // stream: 4, 4
+      {{16, 64, 1, 0.40, 0.34}, 3.6, false},   // rows: 1 x 1 fragments, 4 waves, 4 blocks
+      {{16, 256, 1, 1.09, 1.12}, 3.8, false},  // rows: 1 x 2, 8, 3
+      {{32, 64, 1, 0.47, 0.50}, 4, false},   // rows: 2 x 1, 4, 4
+      {{32, 128, 1, 0.69, 0.76}, 4, false},  // rows: 2 x 1, 8, 3
+      {{32, 256, 1, 1.27, 1.30}, 4.5, false},  // rows: 2 x 4, 4, 3
+      {{64, 256, 1, 2.10, 2.00}, 4.5, false},  // rows: 4 x 2, 8, 2
+      {{128, 128, 2, 2.35, 4.20}, 5, false},
+      {{256, 256, 1, 5.20, 6.70}, 6, false}};
+  static hipError_t launch(int i, const MxGemmArgs& a, const MxProductArgs& p, hipStream_t s) {
+    switch (i) {
+      case 0: return launch_stream<false, false, 2, 8, 1>(a, p, s);
+      case 1: return launch_stream<false, false, 4, 4, 1>(a, p, s);
+      case 2: return launch_rows<false, false, 1, 1, 4, 4>(a, p, s);
+      case 3: return launch_rows<false, false, 1, 2, 8, 3>(a, p, s);
+      case 4: return launch_rows<false, false, 2, 1, 4, 4>(a, p, s);
+      case 5: return launch_rows<false, false, 2, 1, 8, 3>(a, p, s);
+      case 6: return launch_rows<false, false, 2, 4, 4, 3>(a, p, s);
+      case 7: return launch_rows<false, false, 4, 2, 8, 2>(a, p, s);
+      case 8: return launch_mx<false, false, 64, 32, 2, 4, 2, false>(a, p, s);
+      default: return launch_mx<false, false, 128, 64, 2, 4, 2, true>(a, p, s);
+    }
+  }
+};
+template <>
+struct Shapes<false, true> {
+  static constexpr Shape all[] = {
+      {{16, 16, 1, 0.36, 0.40}, 3.3, false},
+      {{16, 32, 1, 0.49, 0.50}, 3.4, true},
+      {{16, 32, 1, 0.48, 0.34}, 3.8, false},
+      {{16, 128, 1, 1.11, 1.14}, 4.5, true},
+      {{32, 64, 1, 0.85, 0.70}, 4, false},
+      {{32, 128, 1, 1.30, 1.31}, 5, true},
+      {{64, 128, 1, 2.10, 1.91}, 5, false},
+      {{128, 64, 2, 2.65, 4.60}, 6, false},
+      {{256, 128, 1, 5.70, 6.95}, 7, true}};
+  static hipError_t launch(int i, const MxGemmArgs& a, const MxProductArgs& p, hipStream_t s) {
+    switch (i) {
+      case 0: return launch_stream<false, true, 2, 8, 1>(a, p, s);
+      case 1: return launch_stream<false, true, 4, 4, 1>(a, p, s);
+      case 2: return launch_rows<false, true, 1, 2, 2, 4>(a, p, s);
+      case 3: return launch_rows<false, true, 1, 4, 4, 3>(a, p, s);
+      case 4: return launch_rows<false, true, 2, 2, 4, 3>(a, p, s);
+      case 5: return launch_rows<false, true, 2, 4, 4, 3>(a, p, s);
+      case 6: return launch_rows<false, true, 4, 2, 8, 2>(a, p, s);
+      case 7: return launch_mx<false, true, 64, 32, 2, 4, 2, false>(a, p, s);
+      default: return launch_mx<false, true, 128, 64, 2, 4, 2, true>(a, p, s);
+    }
+  }
+};
+template <>
+struct Shapes<true, false> {
+  static constexpr Shape all[] = {
+      {{16, 32, 1, 0.17, 0.20}, 3.3, false},
+      {{16, 64, 1, 0.31, 0.34}, 3.4, false},
+      {{32, 64, 1, 0.36, 0.31}, 3.6, false},
+      {{32, 128, 1, 0.54, 0.57}, 3.8, false},
+      {{128, 128, 2, 0.77, 1.54}, 4, false},
+      {{256, 256, 1, 1.70, 2.65}, 6, false}};
+  static hipError_t launch(int i, const MxGemmArgs& a, const MxProductArgs& p, hipStream_t s) {
+    switch (i) {
+      case 0: return launch_stream<true, false, 2, 4, 1>(a, p, s);
+      case 1: return launch_stream<true, false, 4, 4, 1>(a, p, s);
+      case 2: return launch_rows<true, false, 2, 1, 4, 4>(a, p, s);
+      case 3: return launch_rows<true, false, 2, 2, 4, 3>(a, p, s);
+      case 4: return launch_mx<true, false, 64, 64, 2, 2, 2, true>(a, p, s);
+      default: return launch_mx<true, false, 128, 64, 2, 4, 2, true>(a, p, s);
+    }
+  }
+};
+template <>
+struct Shapes<true, true> {
+  static constexpr Shape all[] = {
+      {{16, 16, 1, 0.19, 0.22}, 3.3, false},
+      {{16, 32, 1, 0.31, 0.33}, 3.4, true},
+      {{32, 32, 1, 0.34, 0.31}, 3.6, false},
+      {{32, 64, 1, 0.54, 0.56}, 3.8, false},
+      {{32, 128, 1, 1.08, 1.09}, 5, true},
+      {{128, 64, 2, 0.97, 1.70}, 6, true},
+      {{256, 128, 1, 2.15, 3.00}, 7, true}};
+  static hipError_t launch(int i, const MxGemmArgs& a, const MxProductArgs& p, hipStream_t s) {
+    switch (i) {
+      case 0: return launch_stream<true, true, 2, 8, 1>(a, p, s);
+      case 1: return launch_stream<true, true, 4, 4, 1>(a, p, s);
+      case 2: return launch_rows<true, true, 2, 2, 2, 4>(a, p, s);
+      case 3: return launch_rows<true, true, 2, 2, 4, 3>(a, p, s);
+      case 4: return launch_rows<true, true, 2, 4, 4, 3>(a, p, s);
+      case 5: return launch_mx<true, true, 64, 64, 2, 2, 2, true>(a, p, s);
+      default: return launch_mx<true, true, 128, 64, 2, 4, 2, true>(a, p, s);
+    }
+  }
+};
+
+// (at most 512 threads a workgroup)
+bool tiles_fit(const GroupedGemmArgs& g, const TileCost& c) {
+  return xcd_grid(tile_items(kForward, g, c.TM, c.TN)) <= kMaxWorkgroups / 2;
+}
+
+// The shape to take, from the sizes alone (the host does not know the offsets): the one that a model of the rounds over the CUs finds
+// fastest, but no faster than the weights' stream.
+template <bool X4, bool PAIR>
+int pick(const MxGemmArgs& a, int cus) {
+  const GroupedGemmArgs& g = a.g;
+  const double active = g.E < g.rows ? g.E : g.rows;
+  const double stream = active * g.N * (PAIR ? 2 : 1) * g.K * (17. / 32) / 5.5e6;  // us
+  const double blocks = mx_blocks(g.K);
+  int best = 0;
+  double least = -1;
+  for (int i = 0; i < (int)(sizeof(Shapes<X4, PAIR>::all) / sizeof(Shape)); ++i) {
+    const Shape& s = Shapes<X4, PAIR>::all[i];
+    if ((a.out_scales && !s.groups) || !tiles_fit(g, s.cost)) continue;
+    const TileCost& c = s.cost;
+    const double work =
+        step_time(kForward, g, TileCost{c.TM, c.TN, c.fit, c.alone * blocks + s.start, c.full * blocks + (c.TM >= 128 ? s.start : 0)}, cus);
+    const double time = std::fmax(work, stream) + 0.1 * work;  // of those that the stream bounds the one with the least work
+    if (least < 0 || time < least) {
+      least = time;
+      best = i;
+    }
+  }
+  return best;
 }
 
 template <bool X4, bool PAIR>
@@ -370,20 +883,17 @@ hipError_t launch_mx_product(const MxGemmArgs& a, hipStream_t stream) {
   const MxProductArgs p{{g.a, g.b, g.a2, g.b2, g.out, g.offsets, g.rows, g.E, g.N, g.K, g.out_bf16 ? 1 : 0, 0,
                          stream_rows(g, kForward)},
                         a.a_scales, a.b_scales, a.b2_scales, a.out_scales};
-  const long long mean = g.rows / g.E;
-  if constexpr (X4) {
-    if (mean >= 128) return launch_mx<true, PAIR, 128, 64, 2, 4, 256, 2, false, true>(a, p, stream);
-    return launch_mx<true, PAIR, 32, 64, 2, 2, 256, 3, true, false>(a, p, stream);
-  } else {
-    if (mean >= 128) return launch_mx<false, PAIR, 128, 64, 2, 4, 64, 3, false, true>(a, p, stream);
-    return launch_mx<false, PAIR, 32, 64, 1, 4, 128, 3, true, false>(a, p, stream);
-  }
+  DeviceInfo dev;
+  const hipError_t e = device_info(&dev);
+  if (e != hipSuccess) return e;
+  return Shapes<X4, PAIR>::launch(pick<X4, PAIR>(a, dev.num_cus), a, p, stream);
 }
 
 }  // namespace
 
+// (the largest tiles: pick passes over those that do not fit)
 bool mx_gemm_fits(const MxGemmArgs& a) {
-  return xcd_grid(tile_items(kForward, a.g, 16, 32)) <= kMaxWorkgroups / 2;
+  return tiles_fit(a.g, a.g.b2 ? TileCost{256, 128, 1, 0, 0} : TileCost{256, 256, 1, 0, 0});
 }
 
 bool mx_ffn_fits(int rows, int E, int d, int d_ff) {
@@ -392,6 +902,7 @@ bool mx_ffn_fits(int rows, int E, int d, int d_ff) {
   up.g.E = down.g.E = E;
   up.g.N = down.g.K = d_ff;
   up.g.K = down.g.N = d;
+  up.g.b2 = &up;  // (a pair)
   return mx_gemm_fits(up) && mx_gemm_fits(down);
 }
 
