@@ -181,20 +181,52 @@ hipError_t launch_tiles(const GroupedGemmArgs& g, const MxDgradArgs& p, hipStrea
   return hipGetLastError();
 }
 
+// What a launch may take, and the time of 64 contraction elements (us, see TileCost). From products of 1 to 32,768 rows over 1 to 64
+// experts of 2048 x 4096, two input gradients.
+constexpr TileCost kShapes[] = {
+    {32, 128, 1, 0.40, 0.45}, {32, 128, 2, 0.59, 0.77}, {64, 128, 1, 0.50, 0.52}, {64, 128, 2, 0.73, 0.91},
+    {128, 128, 1, 0.56, 0.72}, {128, 128, 2, 0.84, 1.20}, {256, 256, 1, 1.50, 1.67}};
+hipError_t launch_shape(int i, const GroupedGemmArgs& g, const MxDgradArgs& p, hipStream_t s) {
+  switch (i) {
+    case 0: return launch_tiles<32, 16, 1, 8, 128, 3, false>(g, p, s);
+    case 1: return launch_tiles<32, 32, 1, 4, 64, 3, false>(g, p, s);
+    case 2: return launch_tiles<32, 32, 2, 4, 128, 3, false>(g, p, s);
+    case 3: return launch_tiles<32, 64, 2, 2, 64, 3, false>(g, p, s);
+    case 4: return launch_tiles<64, 32, 2, 4, 128, 2, false>(g, p, s);
+    case 5: return launch_tiles<64, 64, 2, 2, 64, 2, false>(g, p, s);
+    default: return launch_tiles<128, 64, 2, 4, 64, 2, true>(g, p, s);
+  }
+}
+
+// (at most 512 threads a workgroup)
+bool tiles_fit(const GroupedGemmArgs& g, const TileCost& c) {
+  return xcd_grid(tile_items(kDgrad, g, c.TM, c.TN)) <= kMaxWorkgroups / 2;
+}
+
 }  // namespace
 
-bool mx_dgrad_fits(const MxGemmArgs& a) {
-  return xcd_grid(tile_items(kDgrad, a.g, 32, 128)) <= kMaxWorkgroups / 2;
-}
+bool mx_dgrad_fits(const MxGemmArgs& a) { return tiles_fit(a.g, kShapes[sizeof(kShapes) / sizeof(TileCost) - 1]); }
 
 hipError_t launch_mx_dgrad(const MxGemmArgs& a, hipStream_t stream) {
   const GroupedGemmArgs& g = a.g;
   const MxDgradArgs p{{g.a, g.b, g.a2, g.b2, g.out, g.offsets, g.rows, g.E, g.N, g.K, g.out_bf16 ? 1 : 0, 0,
                        stream_rows(g, kDgrad)},
                       a.b_scales, a.b2_scales};
-  const long long mean = g.rows / g.E;
-  if (mean >= 128) return launch_tiles<128, 64, 2, 4, 64, 2, true>(g, p, stream);
-  return launch_tiles<32, 32, 1, 4, 64, 3, false>(g, p, stream);
+  DeviceInfo dev;
+  const hipError_t e = device_info(&dev);
+  if (e != hipSuccess) return e;
+  // The shape that a model of the rounds over the CUs finds fastest.
+  int best = 0;
+  double least = -1;
+  for (int i = 0; i < (int)(sizeof(kShapes) / sizeof(TileCost)); ++i) {
+    if (!tiles_fit(g, kShapes[i])) continue;
+    const double time = step_time(kDgrad, g, kShapes[i], dev.num_cus);
+    if (least < 0 || time < least) {
+      least = time;
+      best = i;
+    }
+  }
+  return launch_shape(best, g, p, stream);
 }
 
 }  // namespace moe
