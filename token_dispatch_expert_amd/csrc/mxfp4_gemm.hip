@@ -743,9 +743,9 @@ hipError_t launch_mx(const MxGemmArgs& a, const MxProductArgs& p, hipStream_t st
   return hipGetLastError();
 }
 
-// What a launch may take, and the time of a block of 256 contraction elements (us): `full` for as many tiles of TM x TN (PAIR: TN
-// columns of h) as the CUs work on at a time, `alone` for a last round with at most one to a CU. `start`: what a tile takes before
-// and after its blocks. From products of 1 to 32,768 rows over 1 to 64 experts, of K = 4096, 2048 and 800.
+// What a launch may take, and the time of a block of 256 contraction elements (us): `alone` for at most one tile of TM x TN (PAIR: TN
+// columns of h) to a CU, `full` for `fit` tiles to each CU, when there are many. `start`: what a tile takes before and after its
+// blocks. From products of 1 to 32,768 rows over 1 to 128 experts, of K = 4096, 2048 and 800.
 struct Shape {
   TileCost cost;
   double start;
@@ -756,8 +756,8 @@ struct Shapes;
 template <>
 struct Shapes<false, false> {
   static constexpr Shape all[] = {
-      {{16, 32, 1, 0.39, 0.40}, 3.3, false},   // stream: 2 fragments, 8 waves
-      {{16, 64, 1, 0.49, 0.50}, 3.4, false},   // stream: 4, 4
+      {{16, 32, 2, 0.36, 0.37}, 3.3, false},   // stream: 2 fragments, 4 waves
+      {{16, 64, 2, 0.49, 0.50}, 3.4, false},   // stream: 4, 4
       {{16, 64, 1, 0.40, 0.34}, 3.6, false},   // rows: 1 x 1 fragments, 4 waves, 4 blocks
       {{16, 256, 1, 1.09, 1.12}, 3.8, false},  // rows: 1 x 2, 8, 3
       {{32, 64, 1, 0.47, 0.50}, 4, false},   // rows: 2 x 1, 4, 4
@@ -768,7 +768,7 @@ struct Shapes<false, false> {
       {{256, 256, 1, 5.20, 6.70}, 6, false}};
   static hipError_t launch(int i, const MxGemmArgs& a, const MxProductArgs& p, hipStream_t s) {
     switch (i) {
-      case 0: return launch_stream<false, false, 2, 8, 1>(a, p, s);
+      case 0: return launch_stream<false, false, 2, 4, 1>(a, p, s);
       case 1: return launch_stream<false, false, 4, 4, 1>(a, p, s);
       case 2: return launch_rows<false, false, 1, 1, 4, 4>(a, p, s);
       case 3: return launch_rows<false, false, 1, 2, 8, 3>(a, p, s);
@@ -784,9 +784,9 @@ struct Shapes<false, false> {
 template <>
 struct Shapes<false, true> {
   static constexpr Shape all[] = {
-      {{16, 16, 1, 0.36, 0.40}, 3.3, false},
-      {{16, 32, 1, 0.49, 0.50}, 3.4, true},
-      {{16, 32, 1, 0.48, 0.34}, 3.8, false},
+      {{16, 16, 2, 0.36, 0.37}, 3.3, false},
+      {{16, 32, 2, 0.49, 0.50}, 3.4, true},
+      {{16, 64, 1, 0.57, 0.59}, 3.8, false},
       {{16, 128, 1, 1.11, 1.14}, 4.5, true},
       {{32, 64, 1, 0.85, 0.70}, 4, false},
       {{32, 128, 1, 1.30, 1.31}, 5, true},
@@ -795,9 +795,9 @@ struct Shapes<false, true> {
       {{256, 128, 1, 5.70, 6.80}, 12, true}};
   static hipError_t launch(int i, const MxGemmArgs& a, const MxProductArgs& p, hipStream_t s) {
     switch (i) {
-      case 0: return launch_stream<false, true, 2, 8, 1>(a, p, s);
+      case 0: return launch_stream<false, true, 2, 4, 1>(a, p, s);
       case 1: return launch_stream<false, true, 4, 4, 1>(a, p, s);
-      case 2: return launch_rows<false, true, 1, 2, 2, 4>(a, p, s);
+      case 2: return launch_rows<false, true, 1, 2, 4, 3>(a, p, s);
       case 3: return launch_rows<false, true, 1, 4, 4, 3>(a, p, s);
       case 4: return launch_rows<false, true, 2, 2, 4, 3>(a, p, s);
       case 5: return launch_rows<false, true, 2, 4, 4, 3>(a, p, s);
@@ -810,8 +810,8 @@ struct Shapes<false, true> {
 template <>
 struct Shapes<true, false> {
   static constexpr Shape all[] = {
-      {{16, 32, 1, 0.17, 0.20}, 3.3, false},
-      {{16, 64, 1, 0.31, 0.34}, 3.4, false},
+      {{16, 32, 2, 0.17, 0.20}, 3.3, false},
+      {{16, 64, 2, 0.31, 0.34}, 3.4, false},
       {{32, 64, 1, 0.36, 0.31}, 3.6, false},
       {{32, 128, 1, 0.54, 0.57}, 3.8, false},
       {{128, 128, 2, 0.77, 1.54}, 4, false},
@@ -830,8 +830,8 @@ struct Shapes<true, false> {
 template <>
 struct Shapes<true, true> {
   static constexpr Shape all[] = {
-      {{16, 16, 1, 0.19, 0.22}, 3.3, false},
-      {{16, 32, 1, 0.31, 0.33}, 3.4, true},
+      {{16, 16, 2, 0.18, 0.21}, 3.3, false},
+      {{16, 32, 2, 0.31, 0.33}, 3.4, true},
       {{32, 32, 1, 0.34, 0.31}, 3.6, false},
       {{32, 64, 1, 0.54, 0.56}, 3.8, false},
       {{32, 128, 1, 1.08, 1.09}, 5, true},
@@ -839,7 +839,7 @@ struct Shapes<true, true> {
       {{256, 128, 1, 2.15, 2.90}, 11, true}};
   static hipError_t launch(int i, const MxGemmArgs& a, const MxProductArgs& p, hipStream_t s) {
     switch (i) {
-      case 0: return launch_stream<true, true, 2, 8, 1>(a, p, s);
+      case 0: return launch_stream<true, true, 2, 4, 1>(a, p, s);
       case 1: return launch_stream<true, true, 4, 4, 1>(a, p, s);
       case 2: return launch_rows<true, true, 2, 2, 2, 4>(a, p, s);
       case 3: return launch_rows<true, true, 2, 2, 4, 3>(a, p, s);
@@ -869,8 +869,16 @@ int pick(const MxGemmArgs& a, int cus) {
     const Shape& s = Shapes<X4, PAIR>::all[i];
     if ((a.out_scales && !s.groups) || !tiles_fit(g, s.cost)) continue;
     const TileCost& c = s.cost;
-    const double work =
-        step_time(kForward, g, TileCost{c.TM, c.TN, c.fit, c.alone * blocks + s.start, c.full * blocks + (c.TM >= 128 ? s.start : 0)}, cus);
+    // Large tiles go over the CUs in rounds. Of the small ones several are on a CU at a time, and a new one starts as one ends; with a
+    // row or two each, `fit` of them to a CU take hardly longer than one.
+    const double tiles = expected_tiles(kForward, g, c.TM, c.TN);
+    double work;
+    if (c.TM >= 128)
+      work = step_time(kForward, g, TileCost{c.TM, c.TN, c.fit, c.alone * blocks + s.start, c.full * blocks + s.start}, cus);
+    else if (c.fit > 1 && g.rows < 4 * active && tiles > cus && tiles <= (double)c.fit * cus)
+      work = s.start + 1.2 * c.alone * blocks;
+    else
+      work = s.start + std::fmax(c.alone, c.full * tiles / cus) * blocks;
     const double time = std::fmax(work, stream) + 0.1 * work;  // of those that the stream bounds the one with the least work
     if (least < 0 || time < least) {
       least = time;
