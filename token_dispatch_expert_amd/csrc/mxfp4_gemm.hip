@@ -105,6 +105,15 @@ __device__ __forceinline__ void issue_scales(const uint8_t* from, int count, cha
   buffer_load_lds4(r, area + load * 256, load * 256 + lane * 4);
 }
 
+// The same for weights in loads of 1 KB: a tile has a multiple of 8 of their rows, so that no lane's 16 bytes cross the last one's
+// end. (4-bit rows: 65,536 by 32 x 2048 x 7168 in 540 - 545 us against 551 - 564, gate and up 1,126 - 1,132 against 1,219 - 1,227.
+// Rows could be read like this but for an odd last one; that gained nothing.)
+constexpr int wide_scale_loads(int n) { return (n * 8 + 1023) / 1024; }
+__device__ __forceinline__ void issue_scales_wide(const uint8_t* from, int count, char* area, int load, int lane) {
+  const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)from, (short)0, count * 8, kBufferWord3);
+  buffer_load_lds16(r, area + load * 1024, load * 1024 + lane * 16, 0);
+}
+
 // h = silu(g) u, in place of the gates. Where the sigmoid is no normal fp32 number (g < kFar, see swiglu.h) it is taken as the
 // fourth power of q = e^(g/4), a factor at a time: u q q is far from both ends of the format unless the result is 0, and the
 // factors' errors ((|g| + 13) 2^-24 in all) are far inside h's rounding.
@@ -221,13 +230,15 @@ __global__ __launch_bounds__(64 * WGM * WGN) void mx_kernel(MxProductArgs a) {
   constexpr int SPB = kMxBlock / DK;        // steps per block
   constexpr int RB = X4 ? RING : 2;         // blocks in LDS
   constexpr int LOADS = OA::kLeast + (X4 ? OB::kLeast : 0);
-  constexpr int LA = X4 ? scale_loads(TM) : 0, LB = scale_loads(PAIR ? TN / 2 : TN), LT = LA + LB * (PAIR ? 2 : 1);
+  // loads of scales, and bytes of their areas
+  constexpr int LA = X4 ? scale_loads(TM) : 0, LB = wide_scale_loads(PAIR ? TN / 2 : TN), LT = LA + LB * (PAIR ? 2 : 1);
+  constexpr int kRowArea = LA * 256, kWeightArea = LB * 1024, kArea = kRowArea + kWeightArea * (PAIR ? 2 : 1);
   static_assert(X4 || RING == 2, "the parts of a block are timed for two slots");
   static_assert(!PAIR || WN % (2 * OB::U) == 0, "a wave holds whole pairs");
-  static_assert(RING * OA::kChunks * 16 + RB * (OB::kChunks * 16 + LT * 256) <= 160 * 1024, "LDS");
+  static_assert(RING * OA::kChunks * 16 + RB * (OB::kChunks * 16 + kArea) <= 160 * 1024, "LDS");
   // (One object: with several, the compiler takes reads of each to depend on the loads into it that are in flight and waits for
   // all of them first. What is read has landed, the kernel's own waits see to that.)
-  __shared__ __align__(16) u32x4 ring[RING * OA::kChunks + RB * (OB::kChunks + LT * 16)];
+  __shared__ __align__(16) u32x4 ring[RING * OA::kChunks + RB * (OB::kChunks + kArea / 16)];
   u32x4* const code_ring = ring + RING * OA::kChunks;
   char* const scale_ring = reinterpret_cast<char*>(code_ring + RB * OB::kChunks);
   const ProductArgs& p = a.p;
@@ -249,14 +260,14 @@ __global__ __launch_bounds__(64 * WGM * WGN) void mx_kernel(MxProductArgs a) {
 
   auto issue_block = [&](int b, int part) __attribute__((always_inline)) {
     if (part == 0) {
-      char* area = scale_ring + b % RB * (LT * 256);
+      char* area = scale_ring + b % RB * kArea;
       const size_t wb = mx_scale_at(t.e, blocks, b, p.N, t.c0);
 #pragma unroll
       for (int i = 0; i < (LT + NW - 1) / NW; ++i) {
         const int l = wave + i * NW;
         if (X4 && l < LA) issue_scales(a.a_scales + mx_scale_at(0, 0, b, p.rows, row0), t.mlim, area, l, lane);
-        else if (l < LA + LB) issue_scales(a.b_scales + wb, t.clim, area + LA * 256, l - LA, lane);
-        else if (PAIR && l < LT) issue_scales(a.b2_scales + wb, t.clim, area + (LA + LB) * 256, l - LA - LB, lane);
+        else if (l < LA + LB) issue_scales_wide(a.b_scales + wb, t.clim, area + kRowArea, l - LA, lane);
+        else if (PAIR && l < LT) issue_scales_wide(a.b2_scales + wb, t.clim, area + kRowArea + kWeightArea, l - LA - LB, lane);
       }
     }
     ob.template issue<0, SPB>(code_ring + b % RB * OB::kChunks, b * 128, K / 2 - b * 128, wave, part);
@@ -288,12 +299,12 @@ __global__ __launch_bounds__(64 * WGM * WGN) void mx_kernel(MxProductArgs a) {
     }
   };
   auto a_scales = [&](int st, int i) __attribute__((always_inline)) {
-    return scales_of(scale_ring + st / SPB % RB * (LT * 256), wm + i * 16, st);
+    return scales_of(scale_ring + st / SPB % RB * kArea, wm + i * 16, st);
   };
   auto b_scales = [&](int st, int j) __attribute__((always_inline)) {
-    const char* area = scale_ring + st / SPB % RB * (LT * 256) + LA * 256;
+    const char* area = scale_ring + st / SPB % RB * kArea + kRowArea;
     const int n = wn + j * 16;
-    if constexpr (PAIR) return scales_of(area + (n / 16 & 1) * (LB * 256), n / 32 * 16, st);
+    if constexpr (PAIR) return scales_of(area + (n / 16 & 1) * kWeightArea, n / 32 * 16, st);
     else return scales_of(area, n, st);
   };
 
