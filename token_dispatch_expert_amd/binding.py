@@ -610,8 +610,8 @@ def _mx(codes, scales, shape, name):
     *lead, rows, d = shape
     if codes.dtype not in _MX_CODE_DT:
         raise TypeError(f"{name}: expected uint8 or float4_e2m1fn_x2, got {codes.dtype}")
-    if scales.dtype not in _MX_SCALE_DT:
-        raise TypeError(f"{name} scales: expected uint8 or float8_e8m0fnu, got {scales.dtype}")
+    if scales is None or scales.dtype not in _MX_SCALE_DT:
+        raise TypeError(f"{name} scales: expected uint8 or float8_e8m0fnu, got {scales.dtype if scales is not None else None}")
     _need(codes, codes.dtype, (*lead, rows, d // 2), name)
     _need(scales, scales.dtype, (*lead, -(-d // 256), rows, 8), name + " scales")
 
