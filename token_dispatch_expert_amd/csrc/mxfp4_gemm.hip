@@ -219,7 +219,7 @@ __device__ __forceinline__ void store_h(const MxProductArgs& a, const TileAt& t,
 // together; bf16 rows have four steps to a block and two blocks, the next of which is loaded in four parts. PAIR: the
 // tile's columns are those of two matrices, 16 of the one and 16 of the other in turn, so that a wave holds gate and up of
 // the same columns of h.
-template <bool X4, bool PAIR, int WM, int WN, int WGM, int WGN, int RING, bool DEAL>
+template <bool X4, bool PAIR, int WM, int WN, int WGM, int WGN, int RING>
 __global__ __launch_bounds__(64 * WGM * WGN) void mx_kernel(MxProductArgs a) {
   constexpr int TM = WM * WGM, TN = WN * WGN, NW = WGM * WGN;
   constexpr int MF = WM / 16, NF = WN / 16;
@@ -243,7 +243,7 @@ __global__ __launch_bounds__(64 * WGM * WGN) void mx_kernel(MxProductArgs a) {
   char* const scale_ring = reinterpret_cast<char*>(code_ring + RB * OB::kChunks);
   const ProductArgs& p = a.p;
   TileAt t;
-  if (!tile_at<kForward, DEAL>(p, TM, PAIR ? TN / 2 : TN, t)) return;
+  if (!tile_at<kForward, true>(p, TM, PAIR ? TN / 2 : TN, t)) return;
   const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WGN * WM, wn = wave % WGN * WN;
@@ -437,14 +437,10 @@ __global__ __launch_bounds__(64 * WGM * WGN) void mx_kernel(MxProductArgs a) {
       for (int i = 0; i < F; ++i) store_fragments<NF>(o, p, acc[i], wm + i * 16, wn, lane);
     }
   };
-  if constexpr (DEAL) {
-    const int mine = __builtin_amdgcn_readfirstlane(min(MF, max(0, (t.mlim - wm + 15) / 16)));
-    static_for<MF + 1>([&](auto c) __attribute__((always_inline)) {
-      if (mine == decltype(c)::value) run(c);
-    });
-  } else {
-    run(std::integral_constant<int, MF>{});
-  }
+  const int mine = __builtin_amdgcn_readfirstlane(min(MF, max(0, (t.mlim - wm + 15) / 16)));
+  static_for<MF + 1>([&](auto c) __attribute__((always_inline)) {
+    if (mine == decltype(c)::value) run(c);
+  });
 }
 
 // Few rows per expert: the weights' codes go straight to registers, DEPTH - 1 blocks of 256 contraction elements ahead, the
@@ -747,10 +743,10 @@ hipError_t launch_stream(const MxGemmArgs& a, const MxProductArgs& p, hipStream_
   return hipGetLastError();
 }
 
-template <bool X4, bool PAIR, int WM, int WN, int WGM, int WGN, int RING, bool DEAL>
+template <bool X4, bool PAIR, int WM, int WN, int WGM, int WGN, int RING>
 hipError_t launch_mx(const MxGemmArgs& a, const MxProductArgs& p, hipStream_t stream) {
   const long long grid = xcd_grid(tile_items(kForward, a.g, WM * WGM, PAIR ? WN * WGN / 2 : WN * WGN));
-  mx_kernel<X4, PAIR, WM, WN, WGM, WGN, RING, DEAL><<<(unsigned)grid, 64 * WGM * WGN, 0, stream>>>(p);
+  mx_kernel<X4, PAIR, WM, WN, WGM, WGN, RING><<<(unsigned)grid, 64 * WGM * WGN, 0, stream>>>(p);
   return hipGetLastError();
 }
 
@@ -775,7 +771,6 @@ struct Shapes<false, false> {
       {{32, 128, 1, 0.69, 0.76}, 4, false},  // rows: 2 x 1, 8, 3
       {{32, 256, 1, 1.27, 1.30}, 4.5, false},  // rows: 2 x 4, 4, 3
       {{64, 256, 1, 2.10, 2.00}, 4.5, false},  // rows: 4 x 2, 8, 2
-      {{128, 128, 2, 2.35, 4.20}, 5, false},
       {{256, 256, 1, 5.20, 6.70}, 6, false}};
   static hipError_t launch(int i, const MxGemmArgs& a, const MxProductArgs& p, hipStream_t s) {
     switch (i) {
@@ -787,8 +782,7 @@ struct Shapes<false, false> {
       case 5: return launch_rows<false, false, 2, 1, 8, 3>(a, p, s);
       case 6: return launch_rows<false, false, 2, 4, 4, 3>(a, p, s);
       case 7: return launch_rows<false, false, 4, 2, 8, 2>(a, p, s);
-      case 8: return launch_mx<false, false, 64, 32, 2, 4, 2, false>(a, p, s);
-      default: return launch_mx<false, false, 128, 64, 2, 4, 2, true>(a, p, s);
+      default: return launch_mx<false, false, 128, 64, 2, 4, 2>(a, p, s);
     }
   }
 };
@@ -802,7 +796,6 @@ struct Shapes<false, true> {
       {{32, 64, 1, 0.85, 0.70}, 4, false},
       {{32, 128, 1, 1.30, 1.31}, 5, true},
       {{64, 128, 1, 2.10, 1.91}, 5, false},
-      {{128, 64, 2, 2.65, 4.60}, 8, false},
       {{256, 128, 1, 5.70, 6.80}, 12, true}};
   static hipError_t launch(int i, const MxGemmArgs& a, const MxProductArgs& p, hipStream_t s) {
     switch (i) {
@@ -813,8 +806,7 @@ struct Shapes<false, true> {
       case 4: return launch_rows<false, true, 2, 2, 4, 3>(a, p, s);
       case 5: return launch_rows<false, true, 2, 4, 4, 3>(a, p, s);
       case 6: return launch_rows<false, true, 4, 2, 8, 2>(a, p, s);
-      case 7: return launch_mx<false, true, 64, 32, 2, 4, 2, false>(a, p, s);
-      default: return launch_mx<false, true, 128, 64, 2, 4, 2, true>(a, p, s);
+      default: return launch_mx<false, true, 128, 64, 2, 4, 2>(a, p, s);
     }
   }
 };
@@ -833,8 +825,8 @@ struct Shapes<true, false> {
       case 1: return launch_stream<true, false, 4, 4, 1>(a, p, s);
       case 2: return launch_rows<true, false, 2, 1, 4, 4>(a, p, s);
       case 3: return launch_rows<true, false, 2, 2, 4, 3>(a, p, s);
-      case 4: return launch_mx<true, false, 64, 64, 2, 2, 2, true>(a, p, s);
-      default: return launch_mx<true, false, 128, 64, 2, 4, 2, true>(a, p, s);
+      case 4: return launch_mx<true, false, 64, 64, 2, 2, 2>(a, p, s);
+      default: return launch_mx<true, false, 128, 64, 2, 4, 2>(a, p, s);
     }
   }
 };
@@ -855,8 +847,8 @@ struct Shapes<true, true> {
       case 2: return launch_rows<true, true, 2, 2, 2, 4>(a, p, s);
       case 3: return launch_rows<true, true, 2, 2, 4, 3>(a, p, s);
       case 4: return launch_rows<true, true, 2, 4, 4, 3>(a, p, s);
-      case 5: return launch_mx<true, true, 64, 64, 2, 2, 2, true>(a, p, s);
-      default: return launch_mx<true, true, 128, 64, 2, 4, 2, true>(a, p, s);
+      case 5: return launch_mx<true, true, 64, 64, 2, 2, 2>(a, p, s);
+      default: return launch_mx<true, true, 128, 64, 2, 4, 2>(a, p, s);
     }
   }
 };
