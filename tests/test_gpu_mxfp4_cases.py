@@ -93,7 +93,7 @@ SIZES = [(8, 8, 0.0, 4096, 1536), (4, 40, 0.0, 2080, 800), (1, 200, 0.0, 2048, 1
          (64, 300, 1.2, 2080, 544), (64, 900, 1.2, 2080, 800), (8, 1200, 0.6, 2080, 544), (1, 1999, 0.0, 2080, 544),
          (32, 3000, 1.2, 2080, 1056), (3, 9000, 0.6, 96, 2080), (3, 30000, 0.6, 1000, 320), (5, 9000, 1.2, 2080, 1056),
          (5, 5, 0.0, 3296, 288), (32, 23683, 0.6, 288, 288), (1, 32048, 0.0, 320, 800), (32, 10978, 0.6, 576, 544), (64, 2850, 0.6, 32, 544),
-         (64, 3648, 0.6, 32, 288)]
+         (64, 3648, 0.6, 32, 288), (64, 757, 0.0, 264, 1184)]
 
 
 def dealt(E, rows, zipf, seed):

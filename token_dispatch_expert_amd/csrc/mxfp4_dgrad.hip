@@ -6,6 +6,7 @@
 // instructions: the codes move a quarter of the bytes from HBM, and the products run at the bf16 rate.
 #include "mxfp4.h"
 #include "mxfp4_internal.h"
+#include "mxfp4_shapes.h"
 #include "product_tiles.h"
 
 namespace moe {
@@ -181,31 +182,146 @@ hipError_t launch_tiles(const GroupedGemmArgs& g, const MxDgradArgs& p, hipStrea
   return hipGetLastError();
 }
 
-// What a launch may take, and the time of 64 contraction elements (us, see TileCost). From products of 1 to 32,768 rows over 1 to 64
-// experts of 2048 x 4096, two input gradients.
-constexpr TileCost kShapes[] = {
-    {32, 128, 1, 0.40, 0.45}, {32, 128, 2, 0.59, 0.77}, {64, 128, 1, 0.50, 0.52}, {64, 128, 2, 0.73, 0.91},
-    {128, 128, 1, 0.56, 0.72}, {128, 128, 2, 0.84, 1.20}, {256, 256, 1, 1.50, 1.67}};
+// Few rows per expert: the codes go straight to registers, and waves share the contraction, wave w steps w, w + NW, .. of 32 rows of W
+// (of the two pairs one after the other). Lane r + 16 g holds, of W's rows 8 g .. 8 g + 7, the same NC dwords of 8 columns
+// each, so that it has 8 contraction elements of each of its columns: converted in pairs of columns, two rows' halves
+// joined by v_perm are what the matrix instructions take, without LDS. Instruction j takes column 8 NC r + j for lane r; a row's
+// load is 64 NC bytes. At the end the waves' sums are joined in order in LDS.
+template <int MF, int NC, int NW>
+__global__ __launch_bounds__(64 * NW) void mx_dgrad_stream_kernel(MxDgradArgs a) {
+  typedef unsigned Dwords __attribute__((ext_vector_type(NC)));
+  constexpr int TM = 16 * MF, TN = 128 * NC, kLaneColumns = 8 * NC, kPitch = TN + 4;
+  constexpr int kOutside = 0x40000000;  // past any extent (at most TM rows of 2^21 bytes)
+  __shared__ __align__(16) float sums[NW][16][kPitch];
+  const ProductArgs& p = a.p;
+  TileAt t;
+  if (!tile_at<kDgrad, false>(p, TM, TN, t)) return;
+  const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int N = t.kdim, ld = p.K / 2, col = t.c0 / 2, dy_ld = N * 2;
+  const size_t row0 = (size_t)t.ra + t.m0;
+  const bool pair = p.a2 != nullptr;
+  const int steps1 = (N + 31) / 32, steps = pair ? 2 * steps1 : steps1;
+  const size_t we = (size_t)t.e * N * ld + col, se = mx_scale_at(t.e, mx_blocks(p.K), t.c0 / kMxBlock, N, 0);
+  const int group = (t.c0 & (kMxBlock - 1)) / kMxGroup + lr * kLaneColumns / kMxGroup;  // of the lane's columns in the block
+
+  struct Step {
+    Dwords c[8];
+    unsigned s[8];
+    u32x4 d[MF];
+  };
+  // step st (past the last: zeros); what columns past K read is in bounds and meets only columns of dx that do not exist
+  auto load = [&](Step& q, int st) __attribute__((always_inline)) {
+    const bool in = st < steps, second = in && st >= steps1;
+    const int k0 = in ? (second ? st - steps1 : st) * 32 : 0, left = in ? min(32, N - k0) : 0;
+    const __amdgpu_buffer_rsrc_t rd = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)(static_cast<const char*>(second ? p.a2 : p.a) + row0 * dy_ld), (short)0, t.mlim * dy_ld, kBufferWord3);
+    const __amdgpu_buffer_rsrc_t rc =
+        __builtin_amdgcn_make_buffer_rsrc((void*)(static_cast<const char*>(second ? p.b2 : p.b) + we + (size_t)k0 * ld),
+                                          (short)0, in ? left * ld - col : 0, kBufferWord3);
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)((second ? a.scales2 : a.scales) + se + (size_t)k0 * 8), (short)0, left * 8, kBufferWord3);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int at = (lg * 8 + i) * ld + lr * (4 * NC);
+      if constexpr (NC == 1) q.c[i][0] = __builtin_amdgcn_raw_buffer_load_b32(rc, at, 0, 0);
+      else q.c[i] = __builtin_amdgcn_raw_buffer_load_b64(rc, at, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q.s[i] = (unsigned char)__builtin_amdgcn_raw_buffer_load_b8(rs, (lg * 8 + i) * 8 + group, 0, 0);
+#pragma unroll
+    for (int f = 0; f < MF; ++f)  // (N is a multiple of 8: a lane's 8 elements all exist, or none)
+      q.d[f] = __builtin_amdgcn_raw_buffer_load_b128(
+          rd, lg * 8 < left ? (f * 16 + lr) * dy_ld + (k0 + lg * 8) * 2 : kOutside, 0, 0);
+  };
+  f32x4 acc[MF][kLaneColumns];
+#pragma unroll
+  for (int f = 0; f < MF; ++f)
+#pragma unroll
+    for (int j = 0; j < kLaneColumns; ++j) acc[f][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto multiply = [&](const Step& q) __attribute__((always_inline)) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      u32x4 v[8];  // of each row the 8 columns
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = __builtin_bit_cast(u32x4, mx_bf16x8(q.c[i][c], mx_scale_f32(q.s[i])));
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        u32x4 w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          w[i] = __builtin_amdgcn_perm(v[2 * i + 1][j / 2], v[2 * i][j / 2], j % 2 ? 0x07060302u : 0x05040100u);
+#pragma unroll
+        for (int f = 0; f < MF; ++f)
+          acc[f][c * 8 + j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              __builtin_bit_cast(bf16x8, w), __builtin_bit_cast(bf16x8, q.d[f]), acc[f][c * 8 + j], 0, 0, 0);
+      }
+    }
+  };
+  Step q;
+  load(q, wave);
+  for (int st = wave; st < steps; st += NW) {
+    multiply(q);
+    load(q, st + NW);
+  }
+#pragma unroll
+  for (int f = 0; f < MF; ++f) {
+    if (f) __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < kLaneColumns; j += 4)
+        *reinterpret_cast<f32x4*>(&sums[wave][lr][(lg * 4 + i) * kLaneColumns + j]) =
+            f32x4{acc[f][j][i], acc[f][j + 1][i], acc[f][j + 2][i], acc[f][j + 3][i]};
+    __syncthreads();
+    // a thread takes 4 columns of a row at a time
+#pragma unroll
+    for (int i = threadIdx.x; i < 16 * TN / 4; i += 64 * NW) {
+      const int r = i / (TN / 4), c = i % (TN / 4) * 4;
+      if (f * 16 + r >= t.mlim || c >= t.clim) continue;
+      f32x4 v = *reinterpret_cast<const f32x4*>(&sums[0][r][c]);
+#pragma unroll
+      for (int w = 1; w < NW; ++w) v += *reinterpret_cast<const f32x4*>(&sums[w][r][c]);
+      const size_t at = (row0 + f * 16 + r) * p.K + t.c0 + c;
+      if (p.out_bf16) *reinterpret_cast<u32x2*>(static_cast<__bf16*>(p.out) + at) = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+      else *reinterpret_cast<f32x4*>(static_cast<float*>(p.out) + at) = v;
+    }
+  }
+}
+
+template <int MF, int NC, int NW>
+hipError_t launch_stream(const GroupedGemmArgs& g, const MxDgradArgs& p, hipStream_t stream) {
+  const long long grid = xcd_grid(tile_items(kDgrad, g, 16 * MF, 128 * NC));
+  mx_dgrad_stream_kernel<MF, NC, NW><<<(unsigned)grid, 64 * NW, 0, stream>>>(p);
+  return hipGetLastError();
+}
+
+// From products of 1 to 32,768 rows over 1 to 64 experts of 2048 x 4096 and 4096 x 1536, one and two input gradients.
+constexpr Shape kShapes[] = {
+    {{16, 128, 1, 0.75, 0.84}, 6, false},  // stream: 16 rows, 1 dword of 8 columns, 8 waves
+    {{16, 256, 1, 1.75, 1.42}, 6, false},  // 2, 4
+    {{16, 256, 1, 1.20, 1.56}, 6, false},  // 2, 8
+    {{32, 128, 1, 0.86, 1.10}, 6, false},  // 32 rows, 1, 8
+    {{32, 256, 1, 1.35, 1.75}, 6, false},  // 2, 8
+    {{128, 128, 1, 1.90, 2.65}, 5, false}, {{128, 128, 2, 2.90, 5.00}, 5, false}, {{256, 256, 1, 5.40, 5.90}, 5, false}};
+constexpr int kShapeCount = sizeof(kShapes) / sizeof(Shape);
 hipError_t launch_shape(int i, const GroupedGemmArgs& g, const MxDgradArgs& p, hipStream_t s) {
   switch (i) {
-    case 0: return launch_tiles<32, 16, 1, 8, 128, 3, false>(g, p, s);
-    case 1: return launch_tiles<32, 32, 1, 4, 64, 3, false>(g, p, s);
-    case 2: return launch_tiles<32, 32, 2, 4, 128, 3, false>(g, p, s);
-    case 3: return launch_tiles<32, 64, 2, 2, 64, 3, false>(g, p, s);
-    case 4: return launch_tiles<64, 32, 2, 4, 128, 2, false>(g, p, s);
-    case 5: return launch_tiles<64, 64, 2, 2, 64, 2, false>(g, p, s);
+    case 0: return launch_stream<1, 1, 8>(g, p, s);
+    case 1: return launch_stream<1, 2, 4>(g, p, s);
+    case 2: return launch_stream<1, 2, 8>(g, p, s);
+    case 3: return launch_stream<2, 1, 8>(g, p, s);
+    case 4: return launch_stream<2, 2, 8>(g, p, s);
+    case 5: return launch_tiles<64, 32, 2, 4, 128, 2, false>(g, p, s);
+    case 6: return launch_tiles<64, 64, 2, 2, 64, 2, false>(g, p, s);
     default: return launch_tiles<128, 64, 2, 4, 64, 2, true>(g, p, s);
   }
 }
 
-// (at most 512 threads a workgroup)
-bool tiles_fit(const GroupedGemmArgs& g, const TileCost& c) {
-  return xcd_grid(tile_items(kDgrad, g, c.TM, c.TN)) <= kMaxWorkgroups / 2;
-}
-
 }  // namespace
 
-bool mx_dgrad_fits(const MxGemmArgs& a) { return tiles_fit(a.g, kShapes[sizeof(kShapes) / sizeof(TileCost) - 1]); }
+// (the largest tiles: the choice passes over those that do not fit)
+bool mx_dgrad_fits(const MxGemmArgs& a) { return shape_fits(kDgrad, a.g, kShapes[kShapeCount - 1].cost); }
 
 hipError_t launch_mx_dgrad(const MxGemmArgs& a, hipStream_t stream) {
   const GroupedGemmArgs& g = a.g;
@@ -215,18 +331,9 @@ hipError_t launch_mx_dgrad(const MxGemmArgs& a, hipStream_t stream) {
   DeviceInfo dev;
   const hipError_t e = device_info(&dev);
   if (e != hipSuccess) return e;
-  // The shape that a model of the rounds over the CUs finds fastest.
-  int best = 0;
-  double least = -1;
-  for (int i = 0; i < (int)(sizeof(kShapes) / sizeof(TileCost)); ++i) {
-    if (!tiles_fit(g, kShapes[i])) continue;
-    const double time = step_time(kDgrad, g, kShapes[i], dev.num_cus);
-    if (least < 0 || time < least) {
-      least = time;
-      best = i;
-    }
-  }
-  return launch_shape(best, g, p, stream);
+  const double pairs = g.b2 ? 2 : 1;
+  const int i = pick_shape(kDgrad, g, kShapes, pairs * g.N * g.K, pairs * g.N / kMxBlock, false, true, dev.num_cus);
+  return launch_shape(i, g, p, stream);
 }
 
 }  // namespace moe

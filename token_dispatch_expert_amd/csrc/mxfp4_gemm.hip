@@ -10,6 +10,7 @@
 // kernel takes the one that gives it whole pieces of memory and few reads of LDS.
 #include "mxfp4.h"
 #include "mxfp4_internal.h"
+#include "mxfp4_shapes.h"
 #include "product_tiles.h"
 #include "swiglu.h"
 
@@ -750,14 +751,7 @@ hipError_t launch_mx(const MxGemmArgs& a, const MxProductArgs& p, hipStream_t st
   return hipGetLastError();
 }
 
-// What a launch may take, and the time of a block of 256 contraction elements (us): `alone` for at most one tile of TM x TN (PAIR: TN
-// columns of h) to a CU, `full` for `fit` tiles to each CU, when there are many. `start`: what a tile takes before and after its
-// blocks. From products of 1 to 32,768 rows over 1 to 128 experts, of K = 4096, 2048 and 800.
-struct Shape {
-  TileCost cost;
-  double start;
-  bool groups;  // a wave holds groups of 32 columns of h, as h in MXFP4 needs
-};
+// From products of 1 to 32,768 rows over 1 to 128 experts, of K = 4096, 2048 and 800.
 template <bool X4, bool PAIR>
 struct Shapes;
 template <>
@@ -853,42 +847,11 @@ struct Shapes<true, true> {
   }
 };
 
-// (at most 512 threads a workgroup)
-bool tiles_fit(const GroupedGemmArgs& g, const TileCost& c) {
-  return xcd_grid(tile_items(kForward, g, c.TM, c.TN)) <= kMaxWorkgroups / 2;
-}
-
-// The shape to take, from the sizes alone (the host does not know the offsets): the one that a model of the rounds over the CUs finds
-// fastest, but no faster than the weights' stream.
 template <bool X4, bool PAIR>
 int pick(const MxGemmArgs& a, int cus) {
   const GroupedGemmArgs& g = a.g;
-  const double active = g.E < g.rows ? g.E : g.rows;
-  const double stream = active * g.N * (PAIR ? 2 : 1) * g.K * (17. / 32) / 5.5e6;  // us
-  const double blocks = mx_blocks(g.K);
-  int best = 0;
-  double least = -1;
-  for (int i = 0; i < (int)(sizeof(Shapes<X4, PAIR>::all) / sizeof(Shape)); ++i) {
-    const Shape& s = Shapes<X4, PAIR>::all[i];
-    if ((a.out_scales && !s.groups) || !tiles_fit(g, s.cost)) continue;
-    const TileCost& c = s.cost;
-    // Large tiles go over the CUs in rounds. Of the small ones several are on a CU at a time, and a new one starts as one ends; with a
-    // row or two each, `fit` of them to a CU take hardly longer than one.
-    const double tiles = expected_tiles(kForward, g, c.TM, c.TN);
-    double work;
-    if (c.TM >= 128)
-      work = step_time(kForward, g, TileCost{c.TM, c.TN, c.fit, c.alone * blocks + s.start, c.full * blocks + s.start}, cus);
-    else if (c.fit > 1 && g.rows < 4 * active && tiles > cus && tiles <= (double)c.fit * cus)
-      work = s.start + 1.2 * c.alone * blocks;
-    else
-      work = s.start + std::fmax(c.alone, c.full * tiles / cus) * blocks;
-    const double time = std::fmax(work, stream) + 0.1 * work;  // of those that the stream bounds the one with the least work
-    if (least < 0 || time < least) {
-      least = time;
-      best = i;
-    }
-  }
-  return best;
+  return pick_shape(kForward, g, Shapes<X4, PAIR>::all, (PAIR ? 2. : 1.) * g.N * g.K, mx_blocks(g.K), a.out_scales != nullptr,
+                    false, cus);
 }
 
 template <bool X4, bool PAIR>
@@ -905,9 +868,9 @@ hipError_t launch_mx_product(const MxGemmArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-// (the largest tiles: pick passes over those that do not fit)
+// (the largest tiles: the choice passes over those that do not fit)
 bool mx_gemm_fits(const MxGemmArgs& a) {
-  return tiles_fit(a.g, a.g.b2 ? TileCost{256, 128, 1, 0, 0} : TileCost{256, 256, 1, 0, 0});
+  return shape_fits(kForward, a.g, a.g.b2 ? TileCost{256, 128, 1, 0, 0} : TileCost{256, 256, 1, 0, 0});
 }
 
 bool mx_ffn_fits(int rows, int E, int d, int d_ff) {
