@@ -50,7 +50,9 @@
  * grouped FFN's tiles load a step of 8 weight rows x 128 bytes at a time, so in these layouts
  * each load reads one contiguous kilobyte instead of 128 bytes of each of 8 rows a row apart;
  * the results are bit-identical to the row-major formats with the same weight values (fp8
- * block scales keep their layout).
+ * block scales keep their layout). MOE_MXFP4, 4-bit codes with a scale byte per 32 elements, for
+ * weights of the FFN and the layer and for rows and weights of the calls that name it: see the
+ * section on it below.
  */
 #ifndef MOE_H
 #define MOE_H
@@ -209,7 +211,7 @@ moe_status_t moe_permute_capped(const void* x, moe_dtype_t x_dtype, const int32_
  * with rows >= 32 * E, or fp8 weights with rows > 8 * E and d and d_ff at most 65536) a
  * 256-byte header and 64 MiB
  * (bf16) or 32 MiB (fp8) of fp32 partial tiles for the last round's tiles, whose contraction is
- * split across workgroups. */
+ * split across workgroups. With MXFP4 weights h alone. */
 size_t moe_ffn_workspace_size(int rows, int E, int d, int d_ff, moe_dtype_t act_dtype,
                               moe_dtype_t w_dtype);
 
@@ -486,7 +488,8 @@ moe_status_t moe_route_backward(const float* dgates, const int32_t* topk_ids,
  *           ((g / 8) * rows + r) * 8 + g % 8. (Scales stored [rows, d/32] elsewhere are brought into this order once.)
  *           Bytes of groups past d (in the last block) are not used.
  * E matrices (weights [E, N, K]) lie one after the other, codes [E, N, K/2] and scales
- * [E, ceil(K/256), N, 8]. The values that the kernels work with are exact in fp32 for every byte, and in bf16 too.
+ * [E, ceil(K/256), N, 8]. Values are exact in fp32 and in bf16, the smallest too; one of 2^128 or more, which needs a
+ * scale of 2^126 or more that no call here writes, may count as infinite.
  * Element counts may pass 2^32; a size whose kernels would need more than 2^32 threads gives MOE_ERR_UNSUPPORTED.
  */
 

@@ -220,6 +220,12 @@ __device__ __forceinline__ void store_h(const MxProductArgs& a, const TileAt& t,
 // together; bf16 rows have four steps to a block and two blocks, the next of which is loaded in four parts. PAIR: the
 // tile's columns are those of two matrices, 16 of the one and 16 of the other in turn, so that a wave holds gate and up of
 // the same columns of h.
+// Many rows per expert. bf16 rows are bound by the matrix instructions and the card's power: 65,536 rows over 32 experts of 2048 x 7168
+// in 1,385 - 1,486 us, 1.30 - 1.39 PFLOP/s, matrix instructions 64% of the cycles at 2.15 GHz, no LDS conflicts; codes take a quarter of
+// the bytes and LDS of bf16 weights. 4-bit rows: 521 - 552 us, 3.5 - 3.7 PFLOP/s, matrix instructions 45%
+// of the cycles: a step of 256 elements is over in 2,048 cycles of them, less than its loads take to arrive from the L2, and LDS holds
+// no third slot of 256 x 256 tiles. (Three slots of smaller tiles 656 - 724 us, four waves of 128 x 128 633; loads issued between the
+// products 977 and more; waves of a SIMD in turn 570, and 1,585 for bf16 rows.) Gate and up of them 1,052 - 1,123 us.
 template <bool X4, bool PAIR, int WM, int WN, int WGM, int WGN, int RING>
 __global__ __launch_bounds__(64 * WGM * WGN) void mx_kernel(MxProductArgs a) {
   constexpr int TM = WM * WGM, TN = WN * WGN, NW = WGM * WGN;
@@ -448,6 +454,9 @@ __global__ __launch_bounds__(64 * WGM * WGN) void mx_kernel(MxProductArgs a) {
 // rows, which all waves share, through a ring of DEPTH slots in LDS. A wave takes MF * 16 rows and NF * 16 columns (PAIR: NF / 2
 // fragments of gate and as many of up), the NW waves of a workgroup neighbouring columns. Of each half of a block (128
 // elements) a lane holds one group of 32 of each of its weight rows, so that a load takes 64 bytes of 16 rows.
+// The weights' stream bounds it: 1,024 rows over 128 experts of 1536 x 4096 (428 MB of weights) in 88 us, 5.0 TB/s with rows
+// and results; of 4096 x 1536 with 4-bit rows 88; gate and up of the former 172. (Tiles of mx_kernel 117; a lane with 512 elements
+// of a row 157; loads that pass the L2 by 101 - 103: both halves of a line are loaded by themselves.)
 template <bool X4, bool PAIR, int MF, int NF, int NW, int DEPTH>
 __global__ __launch_bounds__(64 * NW) void mx_rows_kernel(MxProductArgs a) {
   constexpr int TM = 16 * MF, WN = 16 * NF, TN = WN * NW, TH = PAIR ? TN / 2 : TN, WH = PAIR ? WN / 2 : WN;
@@ -590,6 +599,8 @@ __global__ __launch_bounds__(64 * NW) void mx_rows_kernel(MxProductArgs a) {
 // Few rows and few tiles: no LDS on the operands' way. A workgroup takes 16 rows and NF * 16 columns (PAIR: NF / 2 fragments of
 // gate and as many of up), and its NW waves share the contraction, wave w blocks w, w + NW, .. of 256 elements, in
 // the order of mx_rows_kernel. Blocks are loaded DEPTH ahead; at the end the waves' sums are joined in order in LDS.
+// Latency bounds it: gate and up of one row of 8 of 128 experts of 1536 x 4096 in 15.0 - 16.3 us (54 MB, 11.3 at the rate of a copy), of
+// which an empty launch takes 3; 45.7 in tiles of mx_kernel.
 template <bool X4, bool PAIR, int NF, int NW, int DEPTH>
 __global__ __launch_bounds__(64 * NW) void mx_stream_kernel(MxProductArgs a) {
   constexpr int TN = 16 * NF, TH = PAIR ? TN / 2 : TN, kThreads = 64 * NW, NH = PAIR ? NF / 2 : NF;
