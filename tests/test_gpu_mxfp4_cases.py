@@ -152,3 +152,51 @@ def test_swiglu_sizes(dev, E, rows, zipf, N, K, kind, out):
     moe.moe_grouped_swiglu_mxfp4(x, offsets, w, ws, v, vs, codes, x_scales=xs, h_scales=scales)
     assert (codes[used:] == 0xAB).all() and (scales[:, used:] == 0xAB).all()
     check_mxfp4(codes[:used], scales[:, :used], want, e)
+
+
+@pytest.mark.parametrize("rows", [5, 40, 400])
+def test_few_rows_past_32_bits(dev, rows):
+    """Weights of more than 2^32 elements: the last expert's rows, in the kernels for few rows."""
+    E, N, K = 150, 4104, 7168
+    counts = [0] * (E - 1) + [rows]
+    offsets = ref.offsets_of(counts, dev)
+    w = torch.zeros((E, N, K // 2), dtype=torch.uint8, device=dev)
+    ws = torch.zeros((E, K // 256, N, 8), dtype=torch.uint8, device=dev)
+    last, lasts, wv = held((1, N, K), dev, 1, K ** -0.5)
+    w[-1], ws[-1] = last[0], lasts[0]
+    for kind in ("bf16", "mxfp4"):
+        x, xs, xv = rows_in(kind, rows, K, dev, 2, rows)
+        y = torch.full((rows, N), float("nan"), device=dev)
+        moe.moe_grouped_gemm_mxfp4(x, offsets, w, ws, y, x_scales=xs)
+        want = ref.forward(xv, wv, [rows])
+        e = sum_error(xv, lambda k: wv[0], [(0, 0, rows)], K)
+        within(kind, y, want, e + ref.u(F32) * (want.abs() + e) + 1e-37)
+    dy = rows_in("bf16", rows, N, dev, 3, rows)[0]
+    dx = torch.full((rows, K), float("nan"), device=dev)
+    moe.moe_grouped_gemm_mxfp4_dgrad(dy, offsets, w, ws, dx)
+    want = ref.forward(dy, wv.transpose(1, 2).contiguous(), [rows])
+    e = sum_error(dy, lambda k: wv[0], [(0, 0, rows)], N, axis=0)
+    within("gradient", dx, want, e + ref.u(F32) * (want.abs() + e) + 1e-37)
+
+
+@pytest.mark.parametrize("counts", [[3, 0, 14], [40, 1], [300, 257]], ids=lambda c: "-".join(map(str, c)))
+def test_gradient_of_nan_and_small_scales(dev, counts):
+    """A group of NaN reaches its columns of its expert's rows and nothing else, a row of dy its own row; scales of 2^-127 are exact."""
+    E, N, K, R = len(counts), 264, 800, sum(counts)
+    w, ws, _ = held((E, N, K), dev, 1)
+    ws[E - 1, :, :, :] = torch.where(ws[E - 1] == 255, ws[E - 1], torch.zeros_like(ws[E - 1]))
+    dy = (rows_in("bf16", R, N, dev, 3, R)[0].float() * 2.0 ** 20).to(BF)
+    wv = torch.stack([mx.values(w[k], ws[k]) for k in range(E)])
+    offsets = ref.offsets_of(counts, dev)
+    dx = torch.empty((R, K), device=dev)
+    moe.moe_grouped_gemm_mxfp4_dgrad(dy, offsets, w, ws, dx)
+    want = ref.forward(dy, wv.transpose(1, 2).contiguous(), counts)
+    e = sum_error(dy, lambda k: wv[k], list(ref.spans(counts)), N, axis=0)
+    within("small scales", dx, want, e + ref.u(F32) * (want.abs() + e) + 1e-37)
+    ws[0, 1, 77, 3] = 255          # columns 352 .. 383 of row 77 of the first expert
+    dy[R - 1, 5] = float("nan")
+    moe.moe_grouped_gemm_mxfp4_dgrad(dy, offsets, w, ws, dx)
+    nan = torch.zeros_like(dx, dtype=torch.bool)
+    nan[: counts[0], 352:384] = True
+    nan[R - 1] = True
+    assert torch.equal(torch.isnan(dx), nan)
