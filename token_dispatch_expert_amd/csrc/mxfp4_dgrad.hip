@@ -3,7 +3,8 @@
 // The contraction runs over W's rows, while codes and scales lie along them, so the matrix instructions cannot take the
 // codes as they are stored. A step's weights are converted to bf16 on their way into LDS instead, exactly, where they lie
 // as bf16 weights would, and the transposing LDS reads of the bf16 input gradient bring them to the matrix
-// instructions: the codes move a quarter of the bytes from HBM, and the products run at the bf16 rate.
+// instructions: the codes move a quarter of the bytes from HBM, and the products run at the bf16 rate. With few rows
+// per expert, where a conversion serves few products, the codes do not pass LDS (mx_dgrad_stream_kernel).
 #include "mxfp4.h"
 #include "mxfp4_internal.h"
 #include "mxfp4_shapes.h"
