@@ -50,17 +50,21 @@ struct Tile {
   static constexpr int kTurn = CPR < 16 || kRowsPerLoad * NW >= 16 ? 1 : 16 / (kRowsPerLoad * NW);
   static_assert(CPR >= 16 || kRowsPerLoad * NW % 16 == 0, "the permutation repeats from one load to the next");
   static_assert(!PAIR || T % (2 * U) == 0, "whole pairs of units");
+  static_assert(!PAIR || NW * kRowsPerLoad % (2 * U) == 0, "a wave's loads are all of one matrix");
   static constexpr int kOutside = 0x40000000;  // past any extent (at most 256 rows of 2^21 bytes)
 
-  const char *base, *base2;
+  // PAIR: in the matrix that this wave loads. (Chosen per load between two members, both went to LDS, 32 bytes a thread, and every load
+  // read its descriptor from there and ran in a loop over its lanes' values: 65,536 4-bit rows by 32 x 2048 x 7168 gate and up in
+  // 1,042 - 1,054 us, now 960 - 978; bf16 rows 2,743 - 2,768, now 2,670 - 2,693.)
+  const char* base;
   int extent, ld, row_at, at_in_row;
 
   // first, count: the tile's first row in the matrix (PAIR: in each of the two) and how many exist
   __device__ __forceinline__ void set(const void* origin, const void* origin2, size_t first, int count, int row_bytes,
                                       int wave, int lane) {
     ld = row_bytes;
-    base = static_cast<const char*>(origin) + first * row_bytes;
-    base2 = static_cast<const char*>(origin2) + first * row_bytes;
+    const void* mine = PAIR && (wave * kRowsPerLoad / U & 1) ? origin2 : origin;
+    base = static_cast<const char*>(mine) + first * row_bytes;
     extent = count * row_bytes;
     const int row = lane / CPR, pos = lane % CPR;
     at_in_row = (pos ^ swizzle<CPR, ROT>(wave * kRowsPerLoad + row)) * 16;
@@ -83,8 +87,7 @@ struct Tile {
       const int l = wave + i * NW, r0 = l * kRowsPerLoad;
       if (kLeast < kLoads && l >= kAll) continue;
       const int row0 = PAIR ? (r0 / (2 * U)) * U + r0 % U : r0;
-      const char* b = PAIR && (r0 / U & 1) ? base2 : base;
-      const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)b, (short)0, extent, kBufferWord3);
+      const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)base, (short)0, extent, kBufferWord3);
       buffer_load_lds16<AUX>(r, slot + l * 64, at[i % kTurn] + row0 * ld, byte0);
     }
   }
@@ -225,7 +228,7 @@ __device__ __forceinline__ void store_h(const MxProductArgs& a, const TileAt& t,
 // the bytes and LDS of bf16 weights. 4-bit rows: 521 - 552 us, 3.5 - 3.7 PFLOP/s, matrix instructions 45%
 // of the cycles: a step of 256 elements is over in 2,048 cycles of them, less than its loads take to arrive from the L2, and LDS holds
 // no third slot of 256 x 256 tiles. (Three slots of smaller tiles 656 - 724 us, four waves of 128 x 128 633; loads issued between the
-// products 977 and more; waves of a SIMD in turn 570, and 1,585 for bf16 rows.) Gate and up of them 1,052 - 1,123 us.
+// products 977 and more; waves of a SIMD in turn 570, and 1,585 for bf16 rows.) Gate and up of them 960 - 978 us.
 template <bool X4, bool PAIR, int WM, int WN, int WGM, int WGN, int RING>
 __global__ __launch_bounds__(64 * WGM * WGN) void mx_kernel(MxProductArgs a) {
   constexpr int TM = WM * WGM, TN = WN * WGN, NW = WGM * WGN;
