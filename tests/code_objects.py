@@ -67,7 +67,7 @@ def code(files, containing):
         for part in re.split(r"\n(?=<\S+>:)", text)[1:]:
             name = re.match(r"<(\S+)>:", part)[1]
             if containing in name:
-                found[name] = part
+                found[name] = re.sub(r" *//.*", "", part)  # (the encodings)
     return found
 
 

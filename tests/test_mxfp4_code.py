@@ -1,4 +1,6 @@
 """What the compiler made of the MXFP4 products' kernels: no scratch, and no LDS but what the source counts."""
+import re
+
 import pytest
 
 import code_objects as co
@@ -37,3 +39,18 @@ def test_lds_is_what_the_tiles_take(kernels):
         assert fields["group_segment_fixed_size"] == 2 * tm * 128 + 2 * (tn * 128 + row_scales + weight_scales), name
         seen += 1
     assert seen >= 6
+
+
+def test_blocks_are_loaded_in_turn(files):
+    """The kernels for few rows wait until at most the loads of the later blocks are in flight: that is right while the rows of each
+    block go to LDS before a later block's loads, so no more loads into LDS follow one another than a block has."""
+    seen = 0
+    for name, text in co.code(files, "mx_rows_kernel").items():
+        x4, _, fragments, _, waves, depth = co.template_numbers(name, "mx_rows_kernel")
+        if depth == 2:  # waits for everything
+            continue
+        block = 16 * fragments * (128 if x4 else 512) // 1024 // waves  # of a wave
+        loads = "".join("L" if m[2] else "r" for m in re.finditer(r"^\s*buffer_load_(dwordx[24])\b.*?( lds)?$", text, re.M))
+        assert "r" in loads and max(len(run) for run in loads.split("r")) == block, name
+        seen += 1
+    assert seen >= 14

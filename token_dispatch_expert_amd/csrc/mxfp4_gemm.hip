@@ -560,7 +560,10 @@ __global__ __launch_bounds__(64 * NW) void mx_rows_kernel(MxProductArgs a) {
     };
     Block q[DEPTH];
 #pragma unroll
-    for (int i = 0; i < DEPTH - 1; ++i) load(q[i], i, i);
+    for (int i = 0; i < DEPTH - 1; ++i) {
+      load(q[i], i, i);
+      if constexpr (DEPTH > 2) __atomic_signal_fence(__ATOMIC_SEQ_CST);  // block by block, as the waits count them
+    }
     for (int b0 = 0; b0 < blocks; b0 += DEPTH) {
       static_for<DEPTH>([&](auto ic) __attribute__((always_inline)) {
         constexpr int i = decltype(ic)::value;
