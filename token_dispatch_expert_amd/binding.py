@@ -22,8 +22,11 @@ MOE_F32, MOE_BF16, MOE_FP8_E4M3FN, MOE_BF16_BLOCKED, MOE_FP8_E4M3FN_BLOCKED = 0,
 MOE_MXFP4 = 16
 
 _DTYPE_ENUM = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16,
-               torch.float8_e4m3fn: MOE_FP8_E4M3FN, torch.uint8: MOE_FP8_E4M3FN,
-               torch.float4_e2m1fn_x2: MOE_MXFP4}
+               torch.float8_e4m3fn: MOE_FP8_E4M3FN, torch.uint8: MOE_FP8_E4M3FN}
+# torch's types for pairs of 4-bit codes and for scale bytes, where this torch has them. The FFN and the layer take MXFP4
+# weights as the former (uint8 weights are fp8 there); every MXFP4 call takes both as uint8 too.
+_F4, _E8 = (getattr(torch, n, None) for n in ("float4_e2m1fn_x2", "float8_e8m0fnu"))
+_WEIGHT_ENUM = {**_DTYPE_ENUM, **({_F4: MOE_MXFP4} if _F4 else {})}
 
 ENTRY_POINTS = (
     "moe_status_string", "moe_route", "moe_permute_workspace_size", "moe_permute",
@@ -151,12 +154,12 @@ def moe_permute_workspace_size(T: int, E: int, k: int) -> int:
 
 def moe_ffn_workspace_size(rows: int, E: int, d: int, d_ff: int, act_dtype, w_dtype) -> int:
     return int(load_library().moe_ffn_workspace_size(rows, E, d, d_ff,
-                                                     _DTYPE_ENUM[act_dtype], _DTYPE_ENUM[w_dtype]))
+                                                     _DTYPE_ENUM[act_dtype], _WEIGHT_ENUM[w_dtype]))
 
 
 def moe_layer_workspace_size(T: int, E: int, k: int, d: int, d_ff: int, act_dtype, w_dtype) -> int:
     return int(load_library().moe_layer_workspace_size(T, E, k, d, d_ff, _DTYPE_ENUM[act_dtype],
-                                                       _DTYPE_ENUM[w_dtype]))
+                                                       _WEIGHT_ENUM[w_dtype]))
 
 
 class Workspace:
@@ -263,7 +266,7 @@ def _weights(w_gate, w_up, w_down, s_gate, s_up, s_down, blocked=False):
     tensors keep their [E, d_ff, d] / [E, d, d_ff] shapes. MXFP4 weights are float4_e2m1fn_x2 codes, two to
     an element of the tensors, with their scale bytes."""
     E, d_ff, d = w_gate.shape
-    if w_gate.dtype is torch.float4_e2m1fn_x2:
+    if _WEIGHT_ENUM.get(w_gate.dtype) == MOE_MXFP4:
         if blocked:
             raise TypeError("blocked weights are bfloat16 or float8_e4m3fn")
         d *= 2
@@ -593,8 +596,8 @@ def moe_route_backward(dgates, topk_ids, topk_gates, dlogits, stream=None):
 # ----------------------------------------------------------------------------------------
 # MXFP4: rows and weights in 4 bits (same names as the C ABI)
 # ----------------------------------------------------------------------------------------
-_MX_CODE_DT = (torch.uint8, torch.float4_e2m1fn_x2)
-_MX_SCALE_DT = (torch.uint8, torch.float8_e8m0fnu)
+_MX_CODE_DT = (torch.uint8, _F4)
+_MX_SCALE_DT = (torch.uint8, _E8)
 
 
 def mxfp4_buffers(shape, device="cuda"):
