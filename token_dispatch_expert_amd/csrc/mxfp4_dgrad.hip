@@ -74,15 +74,15 @@ struct Codes {
 // bound it: two gradients of 65,536 rows over 32 experts of 2048 x 7168 in 2.93 - 3.12 ms, 1.23 - 1.31 PFLOP/s, matrix instructions 56%
 // of the cycles at 2.2 GHz; with bf16 weights 3.09 - 3.26. 22% of the cycles are bank conflicts of the converted weights' writes;
 // an order of them without two thirds of those took as long (3,054 - 3,082 against 3,047 - 3,058 us).
-template <int WM, int WN, int WGM, int WGN, int DK, int RING, bool DEAL>
+template <int WM, int WN, int WGM, int WGN, int DK, bool DEAL>
 __global__ __launch_bounds__(64 * WGM * WGN) void mx_dgrad_kernel(MxDgradArgs a) {
   constexpr int TM = WM * WGM, TN = WN * WGN, NW = WGM * WGN;
   constexpr int MF = WM / 16, NF = WN / 16, NS = DK / 32;
   using OA = Operand<false, TM, DK, NW>;
   using OB = Operand<true, TN, DK, NW>;
-  constexpr int STAGE = OA::kChunks + OB::kChunks, LOADS = OA::kLoads;
-  static_assert(RING * STAGE * 16 <= 160 * 1024, "LDS");
-  __shared__ __align__(16) u32x4 ring[RING * STAGE];
+  constexpr int STAGE = OA::kChunks + OB::kChunks, SLOTS = 2;
+  static_assert(SLOTS * STAGE * 16 <= 160 * 1024, "LDS");
+  __shared__ __align__(16) u32x4 ring[SLOTS * STAGE];
   const ProductArgs& p = a.p;
   TileAt t;
   if (!tile_at<kDgrad, DEAL>(p, TM, TN, t)) return;
@@ -102,7 +102,7 @@ __global__ __launch_bounds__(64 * WGM * WGN) void mx_dgrad_kernel(MxDgradArgs a)
 
   auto issue = [&](int st) __attribute__((always_inline)) {
     const bool second = st >= steps1;
-    oa.template issue<0>(ring + st % RING * STAGE, (second ? st - steps1 : st) * DK, t.kdim, second ? moved_a : 0, wave);
+    oa.template issue<0>(ring + st % SLOTS * STAGE, (second ? st - steps1 : st) * DK, t.kdim, second ? moved_a : 0, wave);
   };
   auto load = [&](int st) __attribute__((always_inline)) {
     const bool second = st >= steps1;
@@ -117,13 +117,13 @@ __global__ __launch_bounds__(64 * WGM * WGN) void mx_dgrad_kernel(MxDgradArgs a)
       for (int j = 0; j < NF; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     bf16x8 fa[F ? F : 1], fb[2][NF];
 #pragma unroll
-    for (int r = 0; r < RING; ++r)
+    for (int r = 0; r < SLOTS; ++r)
       if (r < steps) {
         load(r);
         issue(r);
         codes.put(ring + r * STAGE + OA::kChunks);
       }
-    if (RING < steps) load(RING);
+    if (SLOTS < steps) load(SLOTS);
     wait_vmcnt<0>();
     wait_lgkmcnt0();
     bare_barrier();
@@ -132,20 +132,20 @@ __global__ __launch_bounds__(64 * WGM * WGN) void mx_dgrad_kernel(MxDgradArgs a)
 #pragma unroll
     for (int i = 0; i < F; ++i) fa[i] = OA::read(ring, wm + i * 16, 0, lane);
     for (int st = 0; st < steps; ++st) {
-      u32x4* slot = ring + st % RING * STAGE;
-      const u32x4* next = ring + (st + 1) % RING * STAGE;
+      u32x4* slot = ring + st % SLOTS * STAGE;
+      const u32x4* next = ring + (st + 1) % SLOTS * STAGE;
       static_for<NS>([&](auto hc) __attribute__((always_inline)) {
         constexpr int h = decltype(hc)::value, cur = h & 1;
         if (h == NS - 1) {
           wait_lgkmcnt0();  // this wave's reads of step st are back, its weights of later steps written
           if (st + 1 < steps) {
             // step st + 1 has landed for this wave, and after the barrier for all; all are done with step st's slot
-            wait_steps<LOADS, RING - 2>(steps - 2 - st);
+            wait_vmcnt<0>();
             bare_barrier();
-            if (st + RING < steps) {
+            if (st + SLOTS < steps) {
               codes.put(slot + OA::kChunks);
-              if (st + RING + 1 < steps) load(st + RING + 1);
-              issue(st + RING);
+              if (st + SLOTS + 1 < steps) load(st + SLOTS + 1);
+              issue(st + SLOTS);
             }
           }
         }
@@ -179,10 +179,10 @@ __global__ __launch_bounds__(64 * WGM * WGN) void mx_dgrad_kernel(MxDgradArgs a)
   }
 }
 
-template <int WM, int WN, int WGM, int WGN, int DK, int RING, bool DEAL>
+template <int WM, int WN, int WGM, int WGN, int DK, bool DEAL>
 hipError_t launch_tiles(const GroupedGemmArgs& g, const MxDgradArgs& p, hipStream_t stream) {
   const long long grid = xcd_grid(tile_items(kDgrad, g, WM * WGM, WN * WGN));
-  mx_dgrad_kernel<WM, WN, WGM, WGN, DK, RING, DEAL><<<(unsigned)grid, 64 * WGM * WGN, 0, stream>>>(p);
+  mx_dgrad_kernel<WM, WN, WGM, WGN, DK, DEAL><<<(unsigned)grid, 64 * WGM * WGN, 0, stream>>>(p);
   return hipGetLastError();
 }
 
@@ -320,9 +320,9 @@ hipError_t launch_shape(int i, const GroupedGemmArgs& g, const MxDgradArgs& p, h
     case 2: return launch_stream<1, 2, 8>(g, p, s);
     case 3: return launch_stream<2, 1, 8>(g, p, s);
     case 4: return launch_stream<2, 2, 8>(g, p, s);
-    case 5: return launch_tiles<64, 32, 2, 4, 128, 2, false>(g, p, s);
-    case 6: return launch_tiles<64, 64, 2, 2, 64, 2, false>(g, p, s);
-    default: return launch_tiles<128, 64, 2, 4, 64, 2, true>(g, p, s);
+    case 5: return launch_tiles<64, 32, 2, 4, 128, false>(g, p, s);
+    case 6: return launch_tiles<64, 64, 2, 2, 64, false>(g, p, s);
+    default: return launch_tiles<128, 64, 2, 4, 64, true>(g, p, s);
   }
 }
 

@@ -217,10 +217,10 @@ __device__ __forceinline__ void store_h(const MxProductArgs& a, const TileAt& t,
   else store_fragments<NH>(o, a.p, h, r0, c0, lane);
 }
 
-// A workgroup of WGM x WGN waves computes a tile of C, each wave WM x WN of it. Rows go through a ring of RING slots of DK
-// contraction elements in LDS. Codes and their scales go through a ring of blocks of 256 elements, so that a load takes whole
-// lines of a row: X4 (rows in MXFP4) has steps of a block, as many slots as the rows and both operands loaded
-// together; bf16 rows have four steps to a block and two blocks, the next of which is loaded in four parts. PAIR: the
+// A workgroup of WGM x WGN waves computes a tile of C, each wave WM x WN of it. Rows go through two slots of DK
+// contraction elements in LDS, codes and their scales through two slots of blocks of 256 elements, so that a load takes whole
+// lines of a row: X4 (rows in MXFP4) has steps of a block and both operands loaded
+// together; bf16 rows have four steps to a block, and the next block is loaded in four parts. PAIR: the
 // tile's columns are those of two matrices, 16 of the one and 16 of the other in turn, so that a wave holds gate and up of
 // the same columns of h.
 // Many rows per expert. bf16 rows are bound by the matrix instructions and the card's power: 65,536 rows over 32 experts of 2048 x 7168
@@ -229,7 +229,7 @@ __device__ __forceinline__ void store_h(const MxProductArgs& a, const TileAt& t,
 // of the cycles: a step of 256 elements is over in 2,048 cycles of them, less than its loads take to arrive from the L2, and LDS holds
 // no third slot of 256 x 256 tiles. (Three slots of smaller tiles 656 - 724 us, four waves of 128 x 128 633; loads issued between the
 // products 977 and more; waves of a SIMD in turn 570, and 1,585 for bf16 rows.) Gate and up of them 960 - 978 us.
-template <bool X4, bool PAIR, int WM, int WN, int WGM, int WGN, int RING>
+template <bool X4, bool PAIR, int WM, int WN, int WGM, int WGN>
 __global__ __launch_bounds__(64 * WGM * WGN) void mx_kernel(MxProductArgs a) {
   constexpr int TM = WM * WGM, TN = WN * WGN, NW = WGM * WGN;
   constexpr int MF = WM / 16, NF = WN / 16;
@@ -238,19 +238,18 @@ __global__ __launch_bounds__(64 * WGM * WGN) void mx_kernel(MxProductArgs a) {
   using OA = Tile<TM, 128, NW, 1, false>;
   using OB = Tile<TN, 128, NW, 1, PAIR>;
   constexpr int SPB = kMxBlock / DK;        // steps per block
-  constexpr int RB = X4 ? RING : 2;         // blocks in LDS
+  constexpr int SLOTS = 2;
   constexpr int LOADS = OA::kLeast + (X4 ? OB::kLeast : 0);
   // loads of scales, and bytes of their areas
   constexpr int LA = X4 ? scale_loads(TM) : 0, LB = wide_scale_loads(PAIR ? TN / 2 : TN), LT = LA + LB * (PAIR ? 2 : 1);
   constexpr int kRowArea = LA * 256, kWeightArea = LB * 1024, kArea = kRowArea + kWeightArea * (PAIR ? 2 : 1);
-  static_assert(X4 || RING == 2, "the parts of a block are timed for two slots");
   static_assert(!PAIR || WN % (2 * OB::U) == 0, "a wave holds whole pairs");
-  static_assert(RING * OA::kChunks * 16 + RB * (OB::kChunks * 16 + kArea) <= 160 * 1024, "LDS");
+  static_assert(SLOTS * (OA::kChunks * 16 + OB::kChunks * 16 + kArea) <= 160 * 1024, "LDS");
   // (One object: with several, the compiler takes reads of each to depend on the loads into it that are in flight and waits for
   // all of them first. What is read has landed, the kernel's own waits see to that.)
-  __shared__ __align__(16) u32x4 ring[RING * OA::kChunks + RB * (OB::kChunks + kArea / 16)];
-  u32x4* const code_ring = ring + RING * OA::kChunks;
-  char* const scale_ring = reinterpret_cast<char*>(code_ring + RB * OB::kChunks);
+  __shared__ __align__(16) u32x4 ring[SLOTS * (OA::kChunks + OB::kChunks + kArea / 16)];
+  u32x4* const code_ring = ring + SLOTS * OA::kChunks;
+  char* const scale_ring = reinterpret_cast<char*>(code_ring + SLOTS * OB::kChunks);
   const ProductArgs& p = a.p;
   TileAt t;
   if (!tile_at<kForward, true>(p, TM, PAIR ? TN / 2 : TN, t)) return;
@@ -270,7 +269,7 @@ __global__ __launch_bounds__(64 * WGM * WGN) void mx_kernel(MxProductArgs a) {
 
   auto issue_block = [&](int b, int part) __attribute__((always_inline)) {
     if (part == 0) {
-      char* area = scale_ring + b % RB * kArea;
+      char* area = scale_ring + b % SLOTS * kArea;
       const size_t wb = mx_scale_at(t.e, blocks, b, p.N, t.c0);
 #pragma unroll
       for (int i = 0; i < (LT + NW - 1) / NW; ++i) {
@@ -280,7 +279,7 @@ __global__ __launch_bounds__(64 * WGM * WGN) void mx_kernel(MxProductArgs a) {
         else if (PAIR && l < LT) issue_scales_wide(a.b2_scales + wb, t.clim, area + kRowArea + kWeightArea, l - LA - LB, lane);
       }
     }
-    ob.template issue<0, SPB>(code_ring + b % RB * OB::kChunks, b * 128, K / 2 - b * 128, wave, part);
+    ob.template issue<0, SPB>(code_ring + b % SLOTS * OB::kChunks, b * 128, K / 2 - b * 128, wave, part);
   };
   // Rows of step st, and the codes whose turn it is: X4 those of the step; else, once all are done with block q - 1 (the
   // barrier in step 4q - 1, when the rows of step 4q + 1 are issued), one part of block q + 1 with each of steps
@@ -292,7 +291,7 @@ __global__ __launch_bounds__(64 * WGM * WGN) void mx_kernel(MxProductArgs a) {
       const int at = st - 1;
       if (at >= 0 && at / SPB + 1 < blocks) issue_block(at / SPB + 1, at % SPB);
     }
-    oa.template issue<0>(ring + st % RING * OA::kChunks, st * 128, a_bytes - st * 128, wave);
+    oa.template issue<0>(ring + st % SLOTS * OA::kChunks, st * 128, a_bytes - st * 128, wave);
   };
   // Scales of this lane's groups of step st: X4 two, in two bytes; else one. Groups past K hold zeros under whatever their
   // scale bytes are; their scale is taken to be 2^-127, so that zeros they stay.
@@ -309,10 +308,10 @@ __global__ __launch_bounds__(64 * WGM * WGN) void mx_kernel(MxProductArgs a) {
     }
   };
   auto a_scales = [&](int st, int i) __attribute__((always_inline)) {
-    return scales_of(scale_ring + st / SPB % RB * kArea, wm + i * 16, st);
+    return scales_of(scale_ring + st / SPB % SLOTS * kArea, wm + i * 16, st);
   };
   auto b_scales = [&](int st, int j) __attribute__((always_inline)) {
-    const char* area = scale_ring + st / SPB % RB * kArea + kRowArea;
+    const char* area = scale_ring + st / SPB % SLOTS * kArea + kRowArea;
     const int n = wn + j * 16;
     if constexpr (PAIR) return scales_of(area + (n / 16 & 1) * kWeightArea, n / 32 * 16, st);
     else return scales_of(area, n, st);
@@ -333,7 +332,7 @@ __global__ __launch_bounds__(64 * WGM * WGN) void mx_kernel(MxProductArgs a) {
     };
     // The codes of step st, 16 bytes for slice h (X4) or 8 for both slices.
     auto read_codes = [&](int st, int j, int h) __attribute__((always_inline)) {
-      const u32x4* slot = code_ring + st / SPB % RB * OB::kChunks;
+      const u32x4* slot = code_ring + st / SPB % SLOTS * OB::kChunks;
       const int n = wn + j * 16 + lr;
       if constexpr (X4) {
         return OB::read(slot, n, lg * NS + h);
@@ -347,9 +346,9 @@ __global__ __launch_bounds__(64 * WGM * WGN) void mx_kernel(MxProductArgs a) {
     };
     for (int i = 0; i < (X4 ? 0 : SPB); ++i) issue_block(0, i);
 #pragma unroll
-    for (int r = 0; r < RING; ++r)
+    for (int r = 0; r < SLOTS; ++r)
       if (r < steps) issue(r);
-    wait_steps<LOADS, RING - 1>(steps - 1);
+    wait_steps<LOADS, 1>(steps - 1);
     bare_barrier();
     auto product = [&](int i, int j, u32x4 x, auto hc) __attribute__((always_inline)) {
       constexpr int h = decltype(hc)::value;
@@ -378,8 +377,8 @@ __global__ __launch_bounds__(64 * WGM * WGN) void mx_kernel(MxProductArgs a) {
       fa[i] = read_a(ring, i, 0);
     }
     for (int st = 0; st < steps; ++st) {
-      const u32x4* slot = ring + st % RING * OA::kChunks;
-      const u32x4* next = ring + (st + 1) % RING * OA::kChunks;
+      const u32x4* slot = ring + st % SLOTS * OA::kChunks;
+      const u32x4* next = ring + (st + 1) % SLOTS * OA::kChunks;
       static_for<NS>([&](auto hc) __attribute__((always_inline)) {
         constexpr int h = decltype(hc)::value, cur = h & 1;
         constexpr bool last = h == NS - 1;
@@ -387,9 +386,9 @@ __global__ __launch_bounds__(64 * WGM * WGN) void mx_kernel(MxProductArgs a) {
           wait_lgkmcnt0();  // this wave's reads of step st are back
           if (st + 1 < steps) {
             // step st + 1 has landed for this wave, and after the barrier for all; all are done with step st's slot
-            wait_steps<LOADS, RING - 2>(steps - 2 - st);
+            wait_vmcnt<0>();
             bare_barrier();
-            if (st + RING < steps) issue(st + RING);
+            if (st + SLOTS < steps) issue(st + SLOTS);
           }
         }
         // Past the last step these reads bring nothing that is used (any slot, in bounds).
@@ -604,10 +603,11 @@ __global__ __launch_bounds__(64 * NW) void mx_rows_kernel(MxProductArgs a) {
 
 // Few rows and few tiles: no LDS on the operands' way. A workgroup takes 16 rows and NF * 16 columns (PAIR: NF / 2 fragments of
 // gate and as many of up), and its NW waves share the contraction, wave w blocks w, w + NW, .. of 256 elements, in
-// the order of mx_rows_kernel. Blocks are loaded DEPTH ahead; at the end the waves' sums are joined in order in LDS.
+// the order of mx_rows_kernel. A wave issues its next block's loads before a block's products (after them: a row for each of
+// 4 experts of 2048 x 7168 in 9.8 us against 8.7). At the end the waves' sums are joined in order in LDS.
 // Latency bounds it: gate and up of one row of 8 of 128 experts of 1536 x 4096 in 15.0 - 16.3 us (54 MB, 11.3 at the rate of a copy), of
 // which an empty launch takes 3; 45.7 in tiles of mx_kernel.
-template <bool X4, bool PAIR, int NF, int NW, int DEPTH>
+template <bool X4, bool PAIR, int NF, int NW>
 __global__ __launch_bounds__(64 * NW) void mx_stream_kernel(MxProductArgs a) {
   constexpr int TN = 16 * NF, TH = PAIR ? TN / 2 : TN, kThreads = 64 * NW, NH = PAIR ? NF / 2 : NF;
   constexpr int kPitch = TN + 4;
@@ -693,15 +693,12 @@ __global__ __launch_bounds__(64 * NW) void mx_stream_kernel(MxProductArgs a) {
       }
     });
   };
-  Block q[DEPTH];
-#pragma unroll
-  for (int i = 0; i < DEPTH; ++i) load(q[i], wave + i * NW);
-  for (int b = wave; b < blocks; b += DEPTH * NW) {
-#pragma unroll
-    for (int i = 0; i < DEPTH; ++i) {
-      multiply(q[i], b + i * NW);
-      load(q[i], b + (i + DEPTH) * NW);
-    }
+  Block q;
+  load(q, wave);
+  for (int b = wave; b < blocks; b += NW) {
+    const Block now = q;
+    load(q, b + NW);
+    multiply(now, b);
   }
 #pragma unroll
   for (int j = 0; j < NF; ++j) *reinterpret_cast<f32x4*>(&sums[wave][lr][j * 16 + lg * 4]) = acc[j];
@@ -754,17 +751,17 @@ hipError_t launch_rows(const MxGemmArgs& a, const MxProductArgs& p, hipStream_t 
   return hipGetLastError();
 }
 
-template <bool X4, bool PAIR, int NF, int NW, int DEPTH>
+template <bool X4, bool PAIR, int NF, int NW>
 hipError_t launch_stream(const MxGemmArgs& a, const MxProductArgs& p, hipStream_t stream) {
   const long long grid = xcd_grid(tile_items(kForward, a.g, 16, PAIR ? 8 * NF : 16 * NF));
-  mx_stream_kernel<X4, PAIR, NF, NW, DEPTH><<<(unsigned)grid, 64 * NW, 0, stream>>>(p);
+  mx_stream_kernel<X4, PAIR, NF, NW><<<(unsigned)grid, 64 * NW, 0, stream>>>(p);
   return hipGetLastError();
 }
 
-template <bool X4, bool PAIR, int WM, int WN, int WGM, int WGN, int RING>
+template <bool X4, bool PAIR, int WM, int WN, int WGM, int WGN>
 hipError_t launch_mx(const MxGemmArgs& a, const MxProductArgs& p, hipStream_t stream) {
   const long long grid = xcd_grid(tile_items(kForward, a.g, WM * WGM, PAIR ? WN * WGN / 2 : WN * WGN));
-  mx_kernel<X4, PAIR, WM, WN, WGM, WGN, RING><<<(unsigned)grid, 64 * WGM * WGN, 0, stream>>>(p);
+  mx_kernel<X4, PAIR, WM, WN, WGM, WGN><<<(unsigned)grid, 64 * WGM * WGN, 0, stream>>>(p);
   return hipGetLastError();
 }
 
@@ -785,15 +782,15 @@ struct Shapes<false, false> {
       {{256, 256, 1, 5.20, 6.70}, 6, false}};
   static hipError_t launch(int i, const MxGemmArgs& a, const MxProductArgs& p, hipStream_t s) {
     switch (i) {
-      case 0: return launch_stream<false, false, 2, 4, 1>(a, p, s);
-      case 1: return launch_stream<false, false, 4, 4, 1>(a, p, s);
+      case 0: return launch_stream<false, false, 2, 4>(a, p, s);
+      case 1: return launch_stream<false, false, 4, 4>(a, p, s);
       case 2: return launch_rows<false, false, 1, 1, 4, 4>(a, p, s);
       case 3: return launch_rows<false, false, 1, 2, 8, 3>(a, p, s);
       case 4: return launch_rows<false, false, 2, 1, 4, 4>(a, p, s);
       case 5: return launch_rows<false, false, 2, 1, 8, 3>(a, p, s);
       case 6: return launch_rows<false, false, 2, 4, 4, 3>(a, p, s);
       case 7: return launch_rows<false, false, 4, 2, 8, 2>(a, p, s);
-      default: return launch_mx<false, false, 128, 64, 2, 4, 2>(a, p, s);
+      default: return launch_mx<false, false, 128, 64, 2, 4>(a, p, s);
     }
   }
 };
@@ -810,14 +807,14 @@ struct Shapes<false, true> {
       {{256, 128, 1, 5.70, 6.80}, 12, true}};
   static hipError_t launch(int i, const MxGemmArgs& a, const MxProductArgs& p, hipStream_t s) {
     switch (i) {
-      case 0: return launch_stream<false, true, 2, 4, 1>(a, p, s);
-      case 1: return launch_stream<false, true, 4, 4, 1>(a, p, s);
+      case 0: return launch_stream<false, true, 2, 4>(a, p, s);
+      case 1: return launch_stream<false, true, 4, 4>(a, p, s);
       case 2: return launch_rows<false, true, 1, 2, 4, 3>(a, p, s);
       case 3: return launch_rows<false, true, 1, 4, 4, 3>(a, p, s);
       case 4: return launch_rows<false, true, 2, 2, 4, 3>(a, p, s);
       case 5: return launch_rows<false, true, 2, 4, 4, 3>(a, p, s);
       case 6: return launch_rows<false, true, 4, 2, 8, 2>(a, p, s);
-      default: return launch_mx<false, true, 128, 64, 2, 4, 2>(a, p, s);
+      default: return launch_mx<false, true, 128, 64, 2, 4>(a, p, s);
     }
   }
 };
@@ -832,12 +829,12 @@ struct Shapes<true, false> {
       {{256, 256, 1, 1.70, 2.65}, 6, false}};
   static hipError_t launch(int i, const MxGemmArgs& a, const MxProductArgs& p, hipStream_t s) {
     switch (i) {
-      case 0: return launch_stream<true, false, 2, 4, 1>(a, p, s);
-      case 1: return launch_stream<true, false, 4, 4, 1>(a, p, s);
+      case 0: return launch_stream<true, false, 2, 4>(a, p, s);
+      case 1: return launch_stream<true, false, 4, 4>(a, p, s);
       case 2: return launch_rows<true, false, 2, 1, 4, 4>(a, p, s);
       case 3: return launch_rows<true, false, 2, 2, 4, 3>(a, p, s);
-      case 4: return launch_mx<true, false, 64, 64, 2, 2, 2>(a, p, s);
-      default: return launch_mx<true, false, 128, 64, 2, 4, 2>(a, p, s);
+      case 4: return launch_mx<true, false, 64, 64, 2, 2>(a, p, s);
+      default: return launch_mx<true, false, 128, 64, 2, 4>(a, p, s);
     }
   }
 };
@@ -853,13 +850,13 @@ struct Shapes<true, true> {
       {{256, 128, 1, 2.15, 2.90}, 11, true}};
   static hipError_t launch(int i, const MxGemmArgs& a, const MxProductArgs& p, hipStream_t s) {
     switch (i) {
-      case 0: return launch_stream<true, true, 2, 4, 1>(a, p, s);
-      case 1: return launch_stream<true, true, 4, 4, 1>(a, p, s);
+      case 0: return launch_stream<true, true, 2, 4>(a, p, s);
+      case 1: return launch_stream<true, true, 4, 4>(a, p, s);
       case 2: return launch_rows<true, true, 2, 2, 2, 4>(a, p, s);
       case 3: return launch_rows<true, true, 2, 2, 4, 3>(a, p, s);
       case 4: return launch_rows<true, true, 2, 4, 4, 3>(a, p, s);
-      case 5: return launch_mx<true, true, 64, 64, 2, 2, 2>(a, p, s);
-      default: return launch_mx<true, true, 128, 64, 2, 4, 2>(a, p, s);
+      case 5: return launch_mx<true, true, 64, 64, 2, 2>(a, p, s);
+      default: return launch_mx<true, true, 128, 64, 2, 4>(a, p, s);
     }
   }
 };
