@@ -304,15 +304,7 @@ hipError_t launch_stream(const GroupedGemmArgs& g, const MxDgradArgs& p, hipStre
   return hipGetLastError();
 }
 
-// From products of 1 to 32,768 rows over 1 to 64 experts of 2048 x 4096 and 4096 x 1536, one and two input gradients.
-constexpr Shape kShapes[] = {
-    {{16, 128, 1, 0.75, 0.84}, 6, false},  // stream: 16 rows, 1 dword of 8 columns, 8 waves
-    {{16, 256, 1, 1.75, 1.42}, 6, false},  // 2, 4
-    {{16, 256, 1, 1.20, 1.56}, 6, false},  // 2, 8
-    {{32, 128, 1, 0.86, 1.10}, 6, false},  // 32 rows, 1, 8
-    {{32, 256, 1, 1.35, 1.75}, 6, false},  // 2, 8
-    {{128, 128, 1, 1.90, 2.65}, 5, false}, {{128, 128, 2, 2.90, 5.00}, 5, false}, {{256, 256, 1, 5.40, 5.90}, 5, false}};
-constexpr int kShapeCount = sizeof(kShapes) / sizeof(Shape);
+// The shapes of mxfp4_shapes.h, in their order.
 hipError_t launch_shape(int i, const GroupedGemmArgs& g, const MxDgradArgs& p, hipStream_t s) {
   switch (i) {
     case 0: return launch_stream<1, 1, 8>(g, p, s);
@@ -329,7 +321,7 @@ hipError_t launch_shape(int i, const GroupedGemmArgs& g, const MxDgradArgs& p, h
 }  // namespace
 
 // (the largest tiles: the choice passes over those that do not fit)
-bool mx_dgrad_fits(const MxGemmArgs& a) { return shape_fits(kDgrad, a.g, kShapes[kShapeCount - 1].cost); }
+bool mx_dgrad_fits(const MxGemmArgs& a) { return shape_fits(kDgrad, a.g, kDgradShapes[kDgradShapeCount - 1].cost); }
 
 hipError_t launch_mx_dgrad(const MxGemmArgs& a, hipStream_t stream) {
   const GroupedGemmArgs& g = a.g;
@@ -339,9 +331,7 @@ hipError_t launch_mx_dgrad(const MxGemmArgs& a, hipStream_t stream) {
   DeviceInfo dev;
   const hipError_t e = device_info(&dev);
   if (e != hipSuccess) return e;
-  const double pairs = g.b2 ? 2 : 1;
-  const int i = pick_shape(kDgrad, g, kShapes, pairs * g.N * g.K, pairs * g.N / kMxBlock, false, true, dev.num_cus);
-  return launch_shape(i, g, p, stream);
+  return launch_shape(pick_dgrad(g, dev.num_cus), g, p, stream);
 }
 
 }  // namespace moe

@@ -765,107 +765,58 @@ hipError_t launch_mx(const MxGemmArgs& a, const MxProductArgs& p, hipStream_t st
   return hipGetLastError();
 }
 
-// From products of 1 to 32,768 rows over 1 to 128 experts, of K = 4096, 2048 and 800.
+// The shapes of mxfp4_shapes.h, in their order.
 template <bool X4, bool PAIR>
-struct Shapes;
+hipError_t launch_shape(int i, const MxGemmArgs& a, const MxProductArgs& p, hipStream_t s);
 template <>
-struct Shapes<false, false> {
-  static constexpr Shape all[] = {
-      {{16, 32, 2, 0.36, 0.37}, 3.3, false},   // stream: 2 fragments, 4 waves
-      {{16, 64, 2, 0.49, 0.50}, 3.4, false},   // stream: 4, 4
-      {{16, 64, 1, 0.40, 0.34}, 3.6, false},   // rows: 1 x 1 fragments, 4 waves, 4 blocks
-      {{16, 256, 1, 1.09, 1.12}, 3.8, false},  // rows: 1 x 2, 8, 3
-      {{32, 64, 1, 0.47, 0.50}, 4, false},   // rows: 2 x 1, 4, 4
-      {{32, 128, 1, 0.69, 0.76}, 4, false},  // rows: 2 x 1, 8, 3
-      {{32, 256, 1, 1.27, 1.30}, 4.5, false},  // rows: 2 x 4, 4, 3
-      {{64, 256, 1, 2.10, 2.00}, 4.5, false},  // rows: 4 x 2, 8, 2
-      {{256, 256, 1, 5.20, 6.70}, 6, false}};
-  static hipError_t launch(int i, const MxGemmArgs& a, const MxProductArgs& p, hipStream_t s) {
-    switch (i) {
-      case 0: return launch_stream<false, false, 2, 4>(a, p, s);
-      case 1: return launch_stream<false, false, 4, 4>(a, p, s);
-      case 2: return launch_rows<false, false, 1, 1, 4, 4>(a, p, s);
-      case 3: return launch_rows<false, false, 1, 2, 8, 3>(a, p, s);
-      case 4: return launch_rows<false, false, 2, 1, 4, 4>(a, p, s);
-      case 5: return launch_rows<false, false, 2, 1, 8, 3>(a, p, s);
-      case 6: return launch_rows<false, false, 2, 4, 4, 3>(a, p, s);
-      case 7: return launch_rows<false, false, 4, 2, 8, 2>(a, p, s);
-      default: return launch_mx<false, false, 128, 64, 2, 4>(a, p, s);
-    }
+hipError_t launch_shape<false, false>(int i, const MxGemmArgs& a, const MxProductArgs& p, hipStream_t s) {
+  switch (i) {
+    case 0: return launch_stream<false, false, 2, 4>(a, p, s);
+    case 1: return launch_stream<false, false, 4, 4>(a, p, s);
+    case 2: return launch_rows<false, false, 1, 1, 4, 4>(a, p, s);
+    case 3: return launch_rows<false, false, 1, 2, 8, 3>(a, p, s);
+    case 4: return launch_rows<false, false, 2, 1, 4, 4>(a, p, s);
+    case 5: return launch_rows<false, false, 2, 1, 8, 3>(a, p, s);
+    case 6: return launch_rows<false, false, 2, 4, 4, 3>(a, p, s);
+    case 7: return launch_rows<false, false, 4, 2, 8, 2>(a, p, s);
+    default: return launch_mx<false, false, 128, 64, 2, 4>(a, p, s);
   }
-};
+}
 template <>
-struct Shapes<false, true> {
-  static constexpr Shape all[] = {
-      {{16, 16, 2, 0.36, 0.37}, 3.3, false},
-      {{16, 32, 2, 0.49, 0.50}, 3.4, true},
-      {{16, 64, 1, 0.57, 0.59}, 3.8, false},
-      {{16, 128, 1, 1.11, 1.14}, 4.5, true},
-      {{32, 64, 1, 0.85, 0.70}, 4, false},
-      {{32, 128, 1, 1.30, 1.31}, 5, true},
-      {{64, 128, 1, 2.10, 1.91}, 5, false},
-      {{256, 128, 1, 5.70, 6.80}, 12, true}};
-  static hipError_t launch(int i, const MxGemmArgs& a, const MxProductArgs& p, hipStream_t s) {
-    switch (i) {
-      case 0: return launch_stream<false, true, 2, 4>(a, p, s);
-      case 1: return launch_stream<false, true, 4, 4>(a, p, s);
-      case 2: return launch_rows<false, true, 1, 2, 4, 3>(a, p, s);
-      case 3: return launch_rows<false, true, 1, 4, 4, 3>(a, p, s);
-      case 4: return launch_rows<false, true, 2, 2, 4, 3>(a, p, s);
-      case 5: return launch_rows<false, true, 2, 4, 4, 3>(a, p, s);
-      case 6: return launch_rows<false, true, 4, 2, 8, 2>(a, p, s);
-      default: return launch_mx<false, true, 128, 64, 2, 4>(a, p, s);
-    }
+hipError_t launch_shape<false, true>(int i, const MxGemmArgs& a, const MxProductArgs& p, hipStream_t s) {
+  switch (i) {
+    case 0: return launch_stream<false, true, 2, 4>(a, p, s);
+    case 1: return launch_stream<false, true, 4, 4>(a, p, s);
+    case 2: return launch_rows<false, true, 1, 2, 4, 3>(a, p, s);
+    case 3: return launch_rows<false, true, 1, 4, 4, 3>(a, p, s);
+    case 4: return launch_rows<false, true, 2, 2, 4, 3>(a, p, s);
+    case 5: return launch_rows<false, true, 2, 4, 4, 3>(a, p, s);
+    case 6: return launch_rows<false, true, 4, 2, 8, 2>(a, p, s);
+    default: return launch_mx<false, true, 128, 64, 2, 4>(a, p, s);
   }
-};
+}
 template <>
-struct Shapes<true, false> {
-  static constexpr Shape all[] = {
-      {{16, 32, 2, 0.17, 0.20}, 3.3, false},
-      {{16, 64, 2, 0.31, 0.34}, 3.4, false},
-      {{32, 64, 1, 0.36, 0.31}, 3.6, false},
-      {{32, 128, 1, 0.54, 0.57}, 3.8, false},
-      {{128, 128, 2, 0.77, 1.54}, 4, false},
-      {{256, 256, 1, 1.70, 2.65}, 6, false}};
-  static hipError_t launch(int i, const MxGemmArgs& a, const MxProductArgs& p, hipStream_t s) {
-    switch (i) {
-      case 0: return launch_stream<true, false, 2, 4>(a, p, s);
-      case 1: return launch_stream<true, false, 4, 4>(a, p, s);
-      case 2: return launch_rows<true, false, 2, 1, 4, 4>(a, p, s);
-      case 3: return launch_rows<true, false, 2, 2, 4, 3>(a, p, s);
-      case 4: return launch_mx<true, false, 64, 64, 2, 2>(a, p, s);
-      default: return launch_mx<true, false, 128, 64, 2, 4>(a, p, s);
-    }
+hipError_t launch_shape<true, false>(int i, const MxGemmArgs& a, const MxProductArgs& p, hipStream_t s) {
+  switch (i) {
+    case 0: return launch_stream<true, false, 2, 4>(a, p, s);
+    case 1: return launch_stream<true, false, 4, 4>(a, p, s);
+    case 2: return launch_rows<true, false, 2, 1, 4, 4>(a, p, s);
+    case 3: return launch_rows<true, false, 2, 2, 4, 3>(a, p, s);
+    case 4: return launch_mx<true, false, 64, 64, 2, 2>(a, p, s);
+    default: return launch_mx<true, false, 128, 64, 2, 4>(a, p, s);
   }
-};
+}
 template <>
-struct Shapes<true, true> {
-  static constexpr Shape all[] = {
-      {{16, 16, 2, 0.18, 0.21}, 3.3, false},
-      {{16, 32, 2, 0.31, 0.33}, 3.4, true},
-      {{32, 32, 1, 0.34, 0.31}, 3.6, false},
-      {{32, 64, 1, 0.54, 0.56}, 3.8, false},
-      {{32, 128, 1, 1.08, 1.09}, 5, true},
-      {{128, 64, 2, 0.97, 1.70}, 10, true},
-      {{256, 128, 1, 2.15, 2.90}, 11, true}};
-  static hipError_t launch(int i, const MxGemmArgs& a, const MxProductArgs& p, hipStream_t s) {
-    switch (i) {
-      case 0: return launch_stream<true, true, 2, 4>(a, p, s);
-      case 1: return launch_stream<true, true, 4, 4>(a, p, s);
-      case 2: return launch_rows<true, true, 2, 2, 2, 4>(a, p, s);
-      case 3: return launch_rows<true, true, 2, 2, 4, 3>(a, p, s);
-      case 4: return launch_rows<true, true, 2, 4, 4, 3>(a, p, s);
-      case 5: return launch_mx<true, true, 64, 64, 2, 2>(a, p, s);
-      default: return launch_mx<true, true, 128, 64, 2, 4>(a, p, s);
-    }
+hipError_t launch_shape<true, true>(int i, const MxGemmArgs& a, const MxProductArgs& p, hipStream_t s) {
+  switch (i) {
+    case 0: return launch_stream<true, true, 2, 4>(a, p, s);
+    case 1: return launch_stream<true, true, 4, 4>(a, p, s);
+    case 2: return launch_rows<true, true, 2, 2, 2, 4>(a, p, s);
+    case 3: return launch_rows<true, true, 2, 2, 4, 3>(a, p, s);
+    case 4: return launch_rows<true, true, 2, 4, 4, 3>(a, p, s);
+    case 5: return launch_mx<true, true, 64, 64, 2, 2>(a, p, s);
+    default: return launch_mx<true, true, 128, 64, 2, 4>(a, p, s);
   }
-};
-
-template <bool X4, bool PAIR>
-int pick(const MxGemmArgs& a, int cus) {
-  const GroupedGemmArgs& g = a.g;
-  return pick_shape(kForward, g, Shapes<X4, PAIR>::all, (PAIR ? 2. : 1.) * g.N * g.K, mx_blocks(g.K), a.out_scales != nullptr,
-                    false, cus);
 }
 
 template <bool X4, bool PAIR>
@@ -877,7 +828,7 @@ hipError_t launch_mx_product(const MxGemmArgs& a, hipStream_t stream) {
   DeviceInfo dev;
   const hipError_t e = device_info(&dev);
   if (e != hipSuccess) return e;
-  return Shapes<X4, PAIR>::launch(pick<X4, PAIR>(a, dev.num_cus), a, p, stream);
+  return launch_shape<X4, PAIR>(pick_gemm<X4, PAIR>(a, dev.num_cus), a, p, stream);
 }
 
 }  // namespace
