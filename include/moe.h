@@ -485,7 +485,8 @@ moe_status_t moe_route_backward(const float* dgates, const int32_t* topk_ids,
  * code * 2^(b - 127), NaN for b = 255. A matrix of `rows` rows of d elements (d a multiple of 32) is
  *   codes   [rows, d/2] bytes, row-major, element 2i in the low half of byte i;
  *   scales  [ceil(d/256), rows, 8] bytes: the scale of row r, elements 32 g .. 32 g + 31, at
- *           ((g / 8) * rows + r) * 8 + g % 8. (Scales stored [rows, d/32] elsewhere are brought into this order once.)
+ *           ((g / 8) * rows + r) * 8 + g % 8. (Scales stored [rows, d/32] elsewhere, as is usual, are brought into
+ *           this order once, when they are loaded.)
  *           Bytes of groups past d (in the last block) are not used.
  * E matrices (weights [E, N, K]) lie one after the other, codes [E, N, K/2] and scales
  * [E, ceil(K/256), N, 8]. Values are exact in fp32 and in bf16, the smallest too; one of 2^128 or more, which needs a
@@ -502,6 +503,9 @@ moe_status_t moe_route_backward(const float* dgates, const int32_t* topk_ids,
  *           rows that no entry names are left as they were.
  *   The scale is the smallest power of two with which the group's largest magnitude is at most 6, between 2^-125
  *   and 2^125 (1 for a group of zeros); codes are rounded once, to nearest even. (At scale 2^125 codes stop at 6.)
+ *   The OCP specification's own conversion differs: it takes 2^(floor(log2 amax) - 2) and lets values beyond 6
+ *   times that saturate, so that groups whose largest magnitude lies between 6 and 8 times a power of two get
+ *   half this scale there. Bytes of either conversion stand for the same values in every call.
  *   A group that holds a NaN or an infinity gets the scale 255 and codes 0: all of it is NaN.
  */
 moe_status_t moe_mxfp4_quantize(const void* x, moe_dtype_t x_dtype, int E, int rows, int k, int d,

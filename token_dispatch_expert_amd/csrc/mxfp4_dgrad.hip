@@ -71,8 +71,8 @@ struct Codes {
 };
 
 // As tile_kernel of the bf16 products (grouped_gemm.hip), with W through registers. The matrix instructions and the card's power
-// bound it: two gradients of 65,536 rows over 32 experts of 2048 x 7168 in 2.93 - 3.12 ms, 1.23 - 1.31 PFLOP/s, matrix instructions 56%
-// of the cycles at 2.2 GHz; with bf16 weights 3.09 - 3.26. 22% of the cycles are bank conflicts of the converted weights' writes;
+// bound it: two gradients of 65,536 rows over 32 experts of 2048 x 7168 in 2.93 - 3.21 ms over several cards, 1.20 - 1.31 PFLOP/s, matrix
+// instructions 56% of the cycles; with bf16 weights 3.09 - 3.26. 22% of the cycles are bank conflicts of the converted weights' writes;
 // an order of them without two thirds of those took as long (3,054 - 3,082 against 3,047 - 3,058 us).
 template <int WM, int WN, int WGM, int WGN, int DK, bool DEAL>
 __global__ __launch_bounds__(64 * WGM * WGN) void mx_dgrad_kernel(MxDgradArgs a) {
@@ -192,9 +192,9 @@ hipError_t launch_tiles(const GroupedGemmArgs& g, const MxDgradArgs& p, hipStrea
 // joined by v_perm are what the matrix instructions take, without LDS. Instruction j takes column 8 NC r + j for lane r; a row's
 // load is 64 NC bytes. At the end the waves' sums are joined in order in LDS.
 // Two gradients of 64 experts of 2048 x 4096 (570 MB of weights) with a row each take 104 us, 5.5 TB/s, the weights' stream (223 in the best
-// tiles through LDS); 104 rows over 8 experts of 1544 x 800 11.9 us against 21.8, bound by latency: 97 steps over 8 waves, a load's
-// 2 us before the first. Loads a step further ahead gain nothing (122 against 127 us for 128 columns, 110 against 107 for
-// 256): other waves of the CU fill the time.
+// tiles through LDS). There loads a step further ahead gain nothing (122 against 127 us for 128 columns, 110 against 107 for
+// 256): every CU is full and other waves fill the time. 104 rows over 8 experts of 1544 x 800 take 12.2 us against 21.8, bound by
+// latency: 70 workgroups on 256 CUs, whose 8 waves share 98 steps, 12 or 13 loads of a wave one after the other.
 template <int MF, int NC, int NW>
 __global__ __launch_bounds__(64 * NW) void mx_dgrad_stream_kernel(MxDgradArgs a) {
   typedef unsigned Dwords __attribute__((ext_vector_type(NC)));

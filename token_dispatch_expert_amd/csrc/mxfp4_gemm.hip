@@ -101,8 +101,8 @@ struct Tile {
 __device__ __forceinline__ void buffer_load_lds4(__amdgpu_buffer_rsrc_t rsrc, void* lds, int voffset) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (__attribute__((address_space(3))) void*)lds, 4, voffset, 0, 0, 0);
 }
-// The 8 scale bytes of n rows for a block of 256 elements, into an area of kScaleArea(n) bytes: `load` is
-// the number of the 256-byte load.
+// The 8 scale bytes of each of n rows for a block of 256 elements, in scale_loads(n) loads of 256 bytes: `load` is
+// the number of this one.
 constexpr int scale_loads(int n) { return (n * 8 + 255) / 256; }
 __device__ __forceinline__ void issue_scales(const uint8_t* from, int count, char* area, int load, int lane) {
   const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)from, (short)0, count * 8, kBufferWord3);
@@ -110,8 +110,7 @@ __device__ __forceinline__ void issue_scales(const uint8_t* from, int count, cha
 }
 
 // The same for weights in loads of 1 KB: a tile has a multiple of 8 of their rows, so that no lane's 16 bytes cross the last one's
-// end. (4-bit rows: 65,536 by 32 x 2048 x 7168 in 540 - 545 us against 551 - 564, gate and up 1,126 - 1,132 against 1,219 - 1,227.
-// Rows could be read like this but for an odd last one; that gained nothing.)
+// end. (4-bit rows: 65,536 by 32 x 2048 x 7168 in 540 - 545 us against 551 - 564 when it was taken. Rows could be read like this but for an odd last one; that gained nothing.)
 constexpr int wide_scale_loads(int n) { return (n * 8 + 1023) / 1024; }
 __device__ __forceinline__ void issue_scales_wide(const uint8_t* from, int count, char* area, int load, int lane) {
   const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)from, (short)0, count * 8, kBufferWord3);
@@ -224,11 +223,12 @@ __device__ __forceinline__ void store_h(const MxProductArgs& a, const TileAt& t,
 // tile's columns are those of two matrices, 16 of the one and 16 of the other in turn, so that a wave holds gate and up of
 // the same columns of h.
 // Many rows per expert. bf16 rows are bound by the matrix instructions and the card's power: 65,536 rows over 32 experts of 2048 x 7168
-// in 1,385 - 1,486 us, 1.30 - 1.39 PFLOP/s, matrix instructions 64% of the cycles at 2.15 GHz, no LDS conflicts; codes take a quarter of
-// the bytes and LDS of bf16 weights. 4-bit rows: 521 - 552 us, 3.5 - 3.7 PFLOP/s, matrix instructions 45%
+// in 1.41 - 1.50 ms over several cards, 1.28 - 1.36 PFLOP/s, matrix instructions 64% of the cycles, no LDS conflicts; codes take a
+// quarter of the bytes and LDS of bf16 weights. 4-bit rows: 517 - 531 us, 3.6 - 3.7 PFLOP/s, matrix instructions 46%
 // of the cycles: a step of 256 elements is over in 2,048 cycles of them, less than its loads take to arrive from the L2, and LDS holds
 // no third slot of 256 x 256 tiles. (Three slots of smaller tiles 656 - 724 us, four waves of 128 x 128 633; loads issued between the
-// products 977 and more; waves of a SIMD in turn 570, and 1,585 for bf16 rows.) Gate and up of them 960 - 978 us.
+// products 977 and more; waves of a SIMD in turn 570, and 1,585 for bf16 rows.) Gate and up: 0.97 - 1.01 ms with 4-bit rows, also with h
+// in codes, 2.68 - 2.92 with bf16 ones.
 template <bool X4, bool PAIR, int WM, int WN, int WGM, int WGN>
 __global__ __launch_bounds__(64 * WGM * WGN) void mx_kernel(MxProductArgs a) {
   constexpr int TM = WM * WGM, TN = WN * WGN, NW = WGM * WGN;
@@ -459,6 +459,9 @@ __global__ __launch_bounds__(64 * WGM * WGN) void mx_kernel(MxProductArgs a) {
 // The weights' stream bounds it: 1,024 rows over 128 experts of 1536 x 4096 (428 MB of weights) in 88 us, 5.0 TB/s with rows
 // and results; of 4096 x 1536 with 4-bit rows 88; gate and up of the former 172. (Tiles of mx_kernel 117; a lane with 512 elements
 // of a row 157; loads that pass the L2 by 101 - 103: both halves of a line are loaded by themselves.)
+// In some shapes the scales' descriptors end up in vector registers and each of their loads in a loop over the lanes' values. With the
+// extents in scalar registers those loops go, but the compiler then sinks a block's loads behind the products: 32 rows for each
+// of 8 experts of 2048 x 4096 took 19.0 us against 16.1, gate and up of 256 tokens over 128 experts 178 against 168.
 template <bool X4, bool PAIR, int MF, int NF, int NW, int DEPTH>
 __global__ __launch_bounds__(64 * NW) void mx_rows_kernel(MxProductArgs a) {
   constexpr int TM = 16 * MF, WN = 16 * NF, TN = WN * NW, TH = PAIR ? TN / 2 : TN, WH = PAIR ? WN / 2 : WN;
@@ -605,8 +608,8 @@ __global__ __launch_bounds__(64 * NW) void mx_rows_kernel(MxProductArgs a) {
 // gate and as many of up), and its NW waves share the contraction, wave w blocks w, w + NW, .. of 256 elements, in
 // the order of mx_rows_kernel. A wave issues its next block's loads before a block's products (after them: a row for each of
 // 4 experts of 2048 x 7168 in 9.8 us against 8.7). At the end the waves' sums are joined in order in LDS.
-// Latency bounds it: gate and up of one row of 8 of 128 experts of 1536 x 4096 in 15.0 - 16.3 us (54 MB, 11.3 at the rate of a copy), of
-// which an empty launch takes 3; 45.7 in tiles of mx_kernel.
+// Latency bounds it: one row of 8 of 128 experts of 1536 x 4096, gate and up, in 15.6 us with bf16 rows (54 MB, 11.3 at the rate of a copy; an
+// empty launch takes 3; 45.7 in tiles of mx_kernel), 13.7 with 4-bit ones, a product of those 9.1.
 template <bool X4, bool PAIR, int NF, int NW>
 __global__ __launch_bounds__(64 * NW) void mx_stream_kernel(MxProductArgs a) {
   constexpr int TN = 16 * NF, TH = PAIR ? TN / 2 : TN, kThreads = 64 * NW, NH = PAIR ? NF / 2 : NF;
